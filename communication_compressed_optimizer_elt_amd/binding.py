@@ -19,11 +19,17 @@ ABI_VERSION = 1
 CHUNK = 32
 SCHEME_DCT, SCHEME_RANDOM, SCHEME_STRIDE, SCHEME_DILOCO = 0, 1, 2, 3
 VAL_TERNARY, VAL_F16, VAL_F32 = 0, 1, 2
+DTYPE_F32, DTYPE_F16, DTYPE_BF16 = 0, 1, 2
+FMT_E4M3, FMT_E5M2 = 0, 1
+BLOCK = 128
+BLOCK_MAX_K = 1 << 22
+BLOCK_MAX_WORKSPACE = 64 << 20
 OK, EINVAL, EALIGN, EUNSUPPORTED, EHIP, EABI = 0, -1, -2, -3, -4, -5
 
 SYMBOLS = ("demo_abi_version", "demo_strerror", "demo_payload_layout", "demo_encode",
            "demo_decode_apply", "demo_random_select", "demo_encode_adamw", "demo_decode_apply_adamw",
-           "demo_payload_validate")
+           "demo_payload_validate", "demo_dropout", "demo_dropout_backward", "demo_block_layout",
+           "demo_block_quantize", "demo_block_workspace", "demo_block_matmul")
 
 
 class DemoError(RuntimeError):
@@ -61,6 +67,68 @@ class demo_layout(ctypes.Structure):
 class demo_adamw(ctypes.Structure):
     _fields_ = [("beta2", ctypes.c_float), ("eps", ctypes.c_float), ("weight_decay", ctypes.c_float),
                 ("reserved", ctypes.c_uint32)]
+
+
+class demo_dropout_cfg(ctypes.Structure):
+    _fields_ = [("abi_version", ctypes.c_uint32), ("p", ctypes.c_float), ("site", ctypes.c_uint32),
+                ("reserved", ctypes.c_uint32), ("seed", ctypes.c_uint64), ("step", ctypes.c_uint64),
+                ("chunk_offset", ctypes.c_uint64)]
+
+
+class demo_operand(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_uint64) for n in ("pitch", "scale_off", "scale_pitch", "total_bytes")]
+
+    def as_dict(self) -> dict:
+        return {n: int(getattr(self, n)) for n, _ in self._fields_}
+
+
+class demo_block_cfg(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_uint32) for n in ("abi_version", "fmt", "tile", "dtype")]
+
+
+class demo_product_cfg(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_uint32) for n in ("abi_version", "fmt_a", "fmt_b", "dtype")]
+
+
+@dataclass
+class Dropout:
+    """Python view of demo_dropout_cfg."""
+
+    p: float = 0.1
+    seed: int = 0
+    step: int = 0
+    site: int = 0
+    chunk_offset: int = 0
+    abi_version: int = ABI_VERSION
+    reserved: int = 0
+
+    def c(self) -> demo_dropout_cfg:
+        return demo_dropout_cfg(self.abi_version, self.p, self.site, self.reserved, self.seed, self.step,
+                                self.chunk_offset)
+
+
+@dataclass
+class Block:
+    """Python view of demo_block_cfg; the source's type comes from the tensor."""
+
+    fmt: int = FMT_E4M3
+    tile: int = 0
+    abi_version: int = ABI_VERSION
+
+    def c(self, dtype: int) -> demo_block_cfg:
+        return demo_block_cfg(self.abi_version, self.fmt, self.tile, dtype)
+
+
+@dataclass
+class Product:
+    """Python view of demo_product_cfg; the result's type comes from the tensor."""
+
+    fmt_a: int = FMT_E4M3
+    fmt_b: int = FMT_E4M3
+    abi_version: int = ABI_VERSION
+
+    def c(self, dtype: int = DTYPE_F32) -> demo_product_cfg:
+        return demo_product_cfg(self.abi_version, self.fmt_a, self.fmt_b, dtype)
 
 
 @dataclass
@@ -132,6 +200,17 @@ def lib() -> ctypes.CDLL:
         L.demo_decode_apply_adamw.restype = ctypes.c_int
         L.demo_payload_validate.argtypes = [ctypes.POINTER(demo_cfg), ctypes.c_uint64, P, P, P]
         L.demo_payload_validate.restype = ctypes.c_int
+        U32, U64 = ctypes.c_uint32, ctypes.c_uint64
+        drop, prod = ctypes.POINTER(demo_dropout_cfg), ctypes.POINTER(demo_product_cfg)
+        L.demo_dropout.argtypes = [drop, U32, U64, P, P, P, P]
+        L.demo_dropout_backward.argtypes = [drop, U32, U64, P, P, P]
+        L.demo_block_layout.argtypes = [U64, U64, ctypes.POINTER(demo_operand)]
+        L.demo_block_quantize.argtypes = [ctypes.POINTER(demo_block_cfg), U64, U64, P, U64, drop, P, P, P]
+        L.demo_block_workspace.argtypes = [prod, U64, U64, U64, ctypes.POINTER(U64)]
+        L.demo_block_matmul.argtypes = [prod, U64, U64, U64, P, P, P, U64, P, U64, drop, P, U64, P]
+        for name in ("demo_dropout", "demo_dropout_backward", "demo_block_layout", "demo_block_quantize",
+                     "demo_block_workspace", "demo_block_matmul"):
+            getattr(L, name).restype = ctypes.c_int
         if L.demo_abi_version() != ABI_VERSION:
             raise RuntimeError("libdemo.so ABI version mismatch")
         _lib = L
@@ -244,7 +323,8 @@ def demo_payload_validate(cfg, n_elems: int, payload, violations_out, stream=Non
     pb = _payload_bytes(c, n_elems) if _sends(c) else 0
     _check(lib().demo_payload_validate(ctypes.byref(c), n_elems, _buf(payload, "payload", pb),
                                        _buf(violations_out, "violations_out", 8, elem=8), _stream(stream)),
-           "demo_payload_validate")
+           "demo_payload_validate", "demo_dropout", "demo_dropout_backward", "demo_block_layout",
+           "demo_block_quantize", "demo_block_workspace", "demo_block_matmul")
 
 
 def demo_encode_adamw(cfg, adamw, n_elems: int, grad, moment1, moment2, payload_out, q_out=None,
@@ -269,6 +349,120 @@ def demo_decode_apply_adamw(cfg, adamw, n_elems: int, params, moment2, payloads,
                                          _buf(params, "params", nb, True), _buf(moment2, "moment2", nb, True),
                                          _buf(payloads, "payloads", pb), stride, R, _stream(stream)),
            "demo_decode_apply_adamw")
+
+
+_DTYPES = {"torch.float32": DTYPE_F32, "torch.float16": DTYPE_F16, "torch.bfloat16": DTYPE_BF16}
+
+
+def _dtype(t, what: str) -> int:
+    d = _DTYPES.get(str(t.dtype))
+    if d is None:
+        raise TypeError(f"{what}: expected float32, float16 or bfloat16, got {t.dtype}")
+    return d
+
+
+def _here(t, what: str) -> None:
+    """t is on the current device, whose stream the call is queued on."""
+    import torch
+
+    if not t.is_cuda:
+        raise ValueError(f"{what}: expected a device tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{what}: on device {t.device.index}, not the current one")
+
+
+def _flat(t, what: str, like) -> int:
+    """Address of a contiguous tensor with like's type and size."""
+    _here(t, what)
+    if not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous tensor")
+    if t.dtype != like.dtype:
+        raise TypeError(f"{what}: expected {like.dtype}, got {t.dtype}")
+    if t.numel() != like.numel():
+        raise ValueError(f"{what}: holds {t.numel()} elements, not {like.numel()}")
+    return t.data_ptr()
+
+
+def _matrix(t, what: str, shape=None, dtype=None) -> tuple[int, int]:
+    """(address, row pitch) of a matrix with neighbouring columns."""
+    _here(t, what)
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{what}: expected a matrix{'' if shape is None else ' of %d x %d' % tuple(shape)}, "
+                         f"got {tuple(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{what}: expected {dtype}, got {t.dtype}")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{what}: expected neighbouring columns, got stride {t.stride(1)}")
+    if rows > 1 and t.stride(0) < cols:
+        raise ValueError(f"{what}: rows overlap (row stride {t.stride(0)}, {cols} columns)")
+    return t.data_ptr(), t.stride(0) if rows > 1 else max(cols, 1)
+
+
+def _operand_buf(t, what: str, rows: int, cols: int) -> int | None:
+    if t is None:
+        return None
+    _here(t, what)
+    return _buf(t, what, demo_block_layout(rows, cols)["total_bytes"])
+
+
+def _ref(c):
+    return None if c is None else ctypes.byref(c.c() if isinstance(c, Dropout) else c)
+
+
+def demo_dropout(cfg, x, y, residual=None, stream=None) -> None:
+    """y = residual + dropout(x); x, y and residual are contiguous tensors of
+    one type and size."""
+    _check(lib().demo_dropout(_ref(cfg), _dtype(x, "x"), x.numel(), _flat(x, "x", x),
+                              None if residual is None else _flat(residual, "residual", x), _flat(y, "y", x),
+                              _stream(stream)), "demo_dropout")
+
+
+def demo_dropout_backward(cfg, dy, dx, stream=None) -> None:
+    _check(lib().demo_dropout_backward(_ref(cfg), _dtype(dy, "dy"), dy.numel(), _flat(dy, "dy", dy),
+                                       _flat(dx, "dx", dy), _stream(stream)), "demo_dropout_backward")
+
+
+def demo_block_layout(rows: int, cols: int) -> dict:
+    out = demo_operand()
+    _check(lib().demo_block_layout(rows, cols, ctypes.byref(out)), "demo_block_layout")
+    return out.as_dict()
+
+
+def demo_block_quantize(cfg, src, operand=None, operand_t=None, dropout=None, stream=None) -> None:
+    """src: a matrix with neighbouring columns (rows may have a pitch);
+    operand and operand_t: device buffers of demo_block_layout(rows, cols) and
+    demo_block_layout(cols, rows) bytes."""
+    addr, ld = _matrix(src, "src")
+    rows, cols = src.shape
+    c = cfg.c(_dtype(src, "src")) if isinstance(cfg, Block) else cfg
+    _check(lib().demo_block_quantize(ctypes.byref(c), rows, cols, addr, ld, _ref(dropout),
+                                     _operand_buf(operand, "operand", rows, cols),
+                                     _operand_buf(operand_t, "operand_t", cols, rows), _stream(stream)),
+           "demo_block_quantize")
+
+
+def demo_block_workspace(cfg, m: int, n: int, k: int) -> int:
+    out = ctypes.c_uint64()
+    c = cfg.c() if isinstance(cfg, Product) else cfg
+    _check(lib().demo_block_workspace(ctypes.byref(c), m, n, k, ctypes.byref(out)), "demo_block_workspace")
+    return int(out.value)
+
+
+def demo_block_matmul(cfg, m: int, n: int, k: int, a, b, c, addend=None, dropout=None, workspace=None,
+                      stream=None) -> None:
+    """c = addend + dropout(a b^T) for operands a (m x k) and b (n x k); c and
+    addend are m x n matrices of one type with neighbouring columns."""
+    addr, ldc = _matrix(c, "c", (m, n))
+    add, lda = (None, 0) if addend is None else _matrix(addend, "addend", (m, n), c.dtype)
+    cc = cfg.c(_dtype(c, "c")) if isinstance(cfg, Product) else cfg
+    if workspace is not None:
+        _here(workspace, "workspace")
+    _check(lib().demo_block_matmul(ctypes.byref(cc), m, n, k, _operand_buf(a, "a", m, k),
+                                   _operand_buf(b, "b", n, k), addr, ldc, add, lda, _ref(dropout),
+                                   _buf(workspace, "workspace", 0),
+                                   0 if workspace is None else workspace.numel() * workspace.element_size(),
+                                   _stream(stream)), "demo_block_matmul")
 
 
 # raw return codes (tests of the boundary's validation)
@@ -313,3 +507,34 @@ def raw_decode_apply_adamw(cfg, adamw, n_elems, params, moment2, payloads, strid
 def raw_payload_validate(cfg, n_elems, payload, violations_out, stream=0) -> int:
     c = _cfg(cfg)
     return int(lib().demo_payload_validate(ctypes.byref(c), n_elems, payload, violations_out, stream))
+
+
+def raw_dropout(cfg, dtype, n_elems, x, residual, y, stream=0) -> int:
+    return int(lib().demo_dropout(_ref(cfg), dtype, n_elems, x, residual, y, stream))
+
+
+def raw_dropout_backward(cfg, dtype, n_elems, dy, dx, stream=0) -> int:
+    return int(lib().demo_dropout_backward(_ref(cfg), dtype, n_elems, dy, dx, stream))
+
+
+def raw_block_layout(rows, cols) -> tuple[int, dict]:
+    out = demo_operand()
+    rc = int(lib().demo_block_layout(rows, cols, ctypes.byref(out)))
+    return rc, out.as_dict()
+
+
+def raw_block_quantize(cfg, rows, cols, src, ld, dropout, operand, operand_t, stream=0) -> int:
+    return int(lib().demo_block_quantize(None if cfg is None else ctypes.byref(cfg), rows, cols, src, ld,
+                                         _ref(dropout), operand, operand_t, stream))
+
+
+def raw_block_workspace(cfg, m, n, k) -> tuple[int, int]:
+    out = ctypes.c_uint64()
+    rc = int(lib().demo_block_workspace(None if cfg is None else ctypes.byref(cfg), m, n, k, ctypes.byref(out)))
+    return rc, int(out.value)
+
+
+def raw_block_matmul(cfg, m, n, k, a, b, c, ldc, addend=None, ld_addend=0, dropout=None, workspace=None,
+                     workspace_bytes=0, stream=0) -> int:
+    return int(lib().demo_block_matmul(None if cfg is None else ctypes.byref(cfg), m, n, k, a, b, c, ldc, addend,
+                                       ld_addend, _ref(dropout), workspace, workspace_bytes, stream))

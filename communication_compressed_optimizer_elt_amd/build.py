@@ -28,7 +28,7 @@ def build(verbose: bool = False) -> str:
     subprocess.check_call([sys.executable, os.path.join(CSRC, "gen_dct_consts.py")])
     tmp = LIB + ".tmp"
     cmd = [HIPCC, *FLAGS, "-I", os.path.join(ROOT, "include"), "-I", CSRC, "-o", tmp,
-           os.path.join(CSRC, "demo.hip")]
+           os.path.join(CSRC, "demo.hip"), os.path.join(CSRC, "linear.hip")]
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)

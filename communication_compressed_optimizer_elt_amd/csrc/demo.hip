@@ -9,18 +9,22 @@
 #include "decode.hpp"
 #include "demo.h"
 #include "encode.hpp"
+#include "host.hpp"
 
 namespace {
 
 using demo::DecArgs;
 using demo::EncArgs;
+using demo::aligned16;
+using demo::launch;
+using demo::overlap;
+using demo::status_of;
+using demo::up256;
 
 constexpr uint64_t kMaxElems = DEMO_MAX_ELEMS;
 // the one-pass grids of the group kernels (64 work-items per 2048 elements)
 // must stay below 2^32 work-items at the largest shard
 static_assert((kMaxElems / 2048) * 64 < ((uint64_t)1 << 32), "one-pass grid exceeds 2^32 work-items");
-
-uint64_t up256(uint64_t x) { return (x + 255u) & ~(uint64_t)255u; }
 
 bool is_sync_step(const demo_cfg* cfg) { return cfg->step % cfg->period == (uint64_t)(cfg->period - 1); }
 
@@ -84,14 +88,6 @@ void layout_of(const demo_cfg* cfg, uint64_t n, demo_layout* L) {
     L->total_bytes = off;
 }
 
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
-
-bool overlap(const void* a, uint64_t na, const void* b, uint64_t nb) {
-    if (!a || !b || na == 0 || nb == 0) return false;
-    const uintptr_t a0 = (uintptr_t)a, b0 = (uintptr_t)b;
-    return a0 < b0 + nb && b0 < a0 + na;
-}
-
 // One block of 4 waves per 4 consecutive groups; the grid covers the shard
 // once (a one-pass grid streams markedly faster than persistent blocks on
 // MI355X).
@@ -140,24 +136,6 @@ uint32_t shared_mask(const demo_cfg* cfg) {
     if (cfg->scheme == DEMO_SCHEME_DILOCO) return 0xFFFFFFFFu;
     return 0;
 }
-
-template <class T>
-struct same_type {
-    using type = T;
-};
-
-// One kernel launch through hipLaunchKernel, whose return code belongs to this
-// launch alone (hipGetLastError would also report an error that an earlier,
-// unrelated HIP call left pending on the thread).  The parameter types come
-// from the kernel; the arguments are converted to them.
-template <class... P>
-hipError_t launch(void (*kernel)(P...), dim3 grid, dim3 block, size_t lds, hipStream_t s,
-                  typename same_type<P>::type... args) {
-    void* argv[] = {static_cast<void*>(&args)...};
-    return hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, block, argv, lds, s);
-}
-
-int status_of(hipError_t e) { return e == hipSuccess ? DEMO_OK : DEMO_EHIP; }
 
 // AD: Decoupled AdamW (second moment in EncArgs::v / DecArgs::v)
 template <int KS, int VF, bool AD>

@@ -1,0 +1,289 @@
+// linear.hip -- host side of the low-precision linear layer: dropout,
+// block-scaled quantisation and the block-scaled matrix product.
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "demo.h"
+#include "host.hpp"
+#include "product.hpp"
+#include "quantize.hpp"
+
+namespace {
+
+using demo::aligned16;
+using demo::launch;
+using demo::overlap;
+using demo::status_of;
+
+constexpr uint64_t kMaxSide = (uint64_t)1 << 30;  // grids stay below 2^32 work-items, indices below 2^32
+
+uint64_t up(uint64_t x, uint64_t a) { return (x + a - 1) / a * a; }
+
+uint64_t elem_bytes(uint32_t dtype) { return dtype == DEMO_DTYPE_F32 ? 4 : 2; }
+
+bool aligned_to(const void* p, uint64_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+
+bool sides_ok(uint64_t rows, uint64_t cols) {
+    return rows >= 1 && cols >= 1 && rows <= kMaxSide && cols <= kMaxSide && rows * cols <= DEMO_MAX_ELEMS;
+}
+
+demo_operand operand_of(uint64_t rows, uint64_t cols) {
+    demo_operand o{};
+    o.pitch = up(cols, DEMO_BLOCK);
+    o.scale_pitch = up(o.pitch / DEMO_BLOCK, 4);
+    o.scale_off = demo::up256(rows * o.pitch);
+    o.total_bytes = demo::up256(o.scale_off + rows * o.scale_pitch);
+    return o;
+}
+
+// DropArgs of a configuration for n elements, or an error code
+int drop_of(const demo_dropout_cfg* cfg, uint64_t n, demo::Drop* d) {
+    *d = demo::Drop{};
+    if (!cfg) return DEMO_OK;
+    if (cfg->abi_version != DEMO_ABI_VERSION) return DEMO_EABI;
+    if (!(cfg->p >= 0.f && cfg->p <= 1.f) || cfg->site >= (1u << 24) || cfg->reserved != 0) return DEMO_EINVAL;
+    const uint64_t last = (uint64_t)1 << 59;  // the element's number fits 64 bits
+    if (cfg->chunk_offset > last || cfg->chunk_offset + (n + 31) / 32 > last) return DEMO_EINVAL;
+    d->first = cfg->chunk_offset * (DEMO_CHUNK / 8);
+    d->k0 = (uint32_t)cfg->seed;
+    d->k1 = (uint32_t)(cfg->seed >> 32);
+    d->step = (uint32_t)cfg->step;
+    d->c3 = (demo::kTagDropout << 24) | cfg->site;
+    d->threshold = (uint32_t)std::floor((double)cfg->p * 65536.0 + 0.5);
+    d->scale = d->threshold == 65536u ? 0.f : (float)(65536.0 / (65536.0 - (double)d->threshold));
+    d->on = 1;
+    return DEMO_OK;
+}
+
+template <typename T>
+hipError_t launch_dropout(const demo::DropoutArgs& a, hipStream_t s) {
+    const uint64_t blocks = (a.n + 2047) / 2048;
+    const dim3 grid((unsigned)(blocks < (1u << 22) ? blocks : (1u << 22)));
+    return launch(a.residual ? demo::dropout_kernel<T, true> : demo::dropout_kernel<T, false>, grid, dim3(256), 0, s, a);
+}
+
+int dropout_impl(const demo_dropout_cfg* cfg, uint32_t dtype, uint64_t n, const void* x, const void* residual, void* y,
+                 void* hip_stream) {
+    if (!cfg) return DEMO_EINVAL;
+    demo::DropoutArgs a{};
+    if (n == 0 || n > DEMO_MAX_ELEMS) return DEMO_EINVAL;
+    if (const int rc = drop_of(cfg, n, &a.drop)) return rc;
+    if (dtype > DEMO_DTYPE_BF16 || !x || !y) return DEMO_EINVAL;
+    if (!aligned16(x) || !aligned16(y) || (residual && !aligned16(residual))) return DEMO_EALIGN;
+    const uint64_t nb = n * elem_bytes(dtype);
+    if ((x != y && overlap(x, nb, y, nb)) || (residual != y && overlap(residual, nb, y, nb))) return DEMO_EINVAL;
+    a.x = x;
+    a.residual = residual;
+    a.y = y;
+    a.n = n;
+    hipStream_t s = static_cast<hipStream_t>(hip_stream);
+    switch (dtype) {
+    case DEMO_DTYPE_F32: return status_of(launch_dropout<float>(a, s));
+    case DEMO_DTYPE_F16: return status_of(launch_dropout<demo::f16_t>(a, s));
+    default: return status_of(launch_dropout<demo::bf16_t>(a, s));
+    }
+}
+
+template <typename T, int FMT>
+hipError_t launch_quantize(const demo::QuantArgs& a, bool tile, dim3 grid, hipStream_t s) {
+    return launch(tile ? demo::quantize_kernel<T, FMT, true> : demo::quantize_kernel<T, FMT, false>, grid, dim3(256), 0,
+                  s, a);
+}
+
+template <typename T>
+hipError_t launch_quantize(const demo::QuantArgs& a, const demo_block_cfg* cfg, dim3 grid, hipStream_t s) {
+    return cfg->fmt == DEMO_FMT_E4M3 ? launch_quantize<T, demo::kE4M3>(a, cfg->tile != 0, grid, s)
+                                     : launch_quantize<T, demo::kE5M2>(a, cfg->tile != 0, grid, s);
+}
+
+int check_product(const demo_product_cfg* cfg, uint64_t m, uint64_t n, uint64_t k) {
+    if (!cfg) return DEMO_EINVAL;
+    if (cfg->abi_version != DEMO_ABI_VERSION) return DEMO_EABI;
+    if (cfg->fmt_a > DEMO_FMT_E5M2 || cfg->fmt_b > DEMO_FMT_E5M2 || cfg->dtype > DEMO_DTYPE_BF16) return DEMO_EINVAL;
+    if (!sides_ok(m, n) || k < 1) return DEMO_EINVAL;
+    if (k > DEMO_BLOCK_MAX_K) return DEMO_EUNSUPPORTED;
+    if (!sides_ok(m, k) || !sides_ok(n, k)) return DEMO_EINVAL;
+    return DEMO_OK;
+}
+
+constexpr uint64_t kCus = 256;
+constexpr uint64_t kFewRows = 64;
+
+// How a product is cut: tiles of `tile` x `tile` and `splits` of the sum, or
+// (tile 0) the kernel for few rows.
+struct Plan {
+    uint32_t tile;
+    uint32_t splits;
+    uint32_t kb_split;
+};
+
+Plan plan_of(uint64_t m, uint64_t n, uint64_t k) {
+    const uint64_t kb = up(k, DEMO_BLOCK) / DEMO_BLOCK;
+    if (m <= kFewRows) return {0, 1, (uint32_t)kb};
+    const auto tiles = [&](uint64_t t) { return up(m, t) / t * (up(n, t) / t); };
+    if (tiles(256) >= 3 * kCus) return {256, 1, (uint32_t)up(kb, 4)};
+    uint64_t splits = 1;
+    const uint64_t t = tiles(128);
+    if (t <= kCus) {
+        splits = 2 * kCus / t;
+        const uint64_t most = (kb + 7) / 8;  // at least 8 blocks of 128 each
+        if (splits > most) splits = most;
+        while (splits > 1 && splits * m * n * 4 > DEMO_BLOCK_MAX_WORKSPACE) splits--;
+        if (splits < 1) splits = 1;
+    }
+    const uint64_t each = up((kb + splits - 1) / splits, 4);
+    return {128, (uint32_t)((kb + each - 1) / each), (uint32_t)each};
+}
+
+template <int FA, int FB, bool WIDE>
+hipError_t launch_product(demo::ProductArgs a, const Plan& plan, void* workspace, hipStream_t s) {
+    if (plan.tile == 0) {
+        const dim3 grid((a.n + 15) / 16);
+        constexpr int NW = 16;
+        if (a.m <= 16) return launch(demo::product_few_kernel<FA, FB, WIDE, 1, NW>, grid, dim3(64 * NW), 0, s, a);
+        if (a.m <= 32) return launch(demo::product_few_kernel<FA, FB, WIDE, 2, NW>, grid, dim3(64 * NW), 0, s, a);
+        return launch(demo::product_few_kernel<FA, FB, WIDE, 4, 8>, grid, dim3(64 * 8), 0, s, a);
+    }
+    a.kb_split = plan.kb_split;
+    a.partial = plan.splits > 1 ? static_cast<float*>(workspace) : nullptr;
+    a.tiles_m = (a.m + plan.tile - 1) / plan.tile;
+    a.tiles_n = (a.n + plan.tile - 1) / plan.tile;
+    const dim3 grid(a.tiles_m * a.tiles_n, plan.splits);
+    const size_t lds = 2 * (2 * plan.tile) * (DEMO_BLOCK + 4);
+    hipError_t e = plan.tile == 256
+                       ? launch(demo::product_kernel<FA, FB, WIDE, 256, 256, 2, 4>, grid, dim3(512), lds, s, a)
+                       : launch(demo::product_kernel<FA, FB, WIDE, 128, 128, 2, 2>, grid, dim3(256), lds, s, a);
+    if (e != hipSuccess || plan.splits == 1) return e;
+    const uint64_t blocks = ((uint64_t)a.m * ((a.n + 7) / 8) + 255) / 256;
+    return launch(demo::product_join_kernel, dim3((unsigned)(blocks < (1u << 20) ? blocks : (1u << 20))), dim3(256), 0, s,
+                  a, plan.splits);
+}
+
+template <int FA, int FB>
+hipError_t launch_product(const demo::ProductArgs& a, const Plan& plan, void* workspace, hipStream_t s) {
+    return a.dtype == DEMO_DTYPE_F32 ? launch_product<FA, FB, true>(a, plan, workspace, s)
+                                     : launch_product<FA, FB, false>(a, plan, workspace, s);
+}
+
+}  // namespace
+
+extern "C" {
+
+int demo_dropout(const demo_dropout_cfg* cfg, uint32_t dtype, uint64_t n_elems, const void* x, const void* residual,
+                 void* y, void* hip_stream) {
+    return dropout_impl(cfg, dtype, n_elems, x, residual, y, hip_stream);
+}
+
+int demo_dropout_backward(const demo_dropout_cfg* cfg, uint32_t dtype, uint64_t n_elems, const void* dy, void* dx,
+                          void* hip_stream) {
+    return dropout_impl(cfg, dtype, n_elems, dy, nullptr, dx, hip_stream);
+}
+
+int demo_block_layout(uint64_t rows, uint64_t cols, demo_operand* out) {
+    if (!out || !sides_ok(rows, cols)) return DEMO_EINVAL;
+    *out = operand_of(rows, cols);
+    return DEMO_OK;
+}
+
+int demo_block_quantize(const demo_block_cfg* cfg, uint64_t rows, uint64_t cols, const void* src, uint64_t ld,
+                        const demo_dropout_cfg* dropout, void* operand, void* operand_t, void* hip_stream) {
+    if (!cfg) return DEMO_EINVAL;
+    if (cfg->abi_version != DEMO_ABI_VERSION) return DEMO_EABI;
+    if (cfg->fmt > DEMO_FMT_E5M2 || cfg->tile > 1 || cfg->dtype > DEMO_DTYPE_BF16) return DEMO_EINVAL;
+    if (!sides_ok(rows, cols) || ld < cols || ld > DEMO_MAX_ELEMS) return DEMO_EINVAL;
+    demo::QuantArgs a{};
+    if (const int rc = drop_of(dropout, rows * cols, &a.drop)) return rc;
+    if (!src || (!operand && !operand_t)) return DEMO_EINVAL;
+    const uint64_t eb = elem_bytes(cfg->dtype);
+    if (!aligned_to(src, eb) || !aligned16(operand) || !aligned16(operand_t)) return DEMO_EALIGN;
+    const demo_operand o = operand_of(rows, cols), t = operand_of(cols, rows);
+    const uint64_t nb = ((rows - 1) * ld + cols) * eb;
+    if (overlap(src, nb, operand, o.total_bytes) || overlap(src, nb, operand_t, t.total_bytes) ||
+        overlap(operand, o.total_bytes, operand_t, t.total_bytes))
+        return DEMO_EINVAL;
+    a.src = src;
+    a.ld = ld;
+    a.rows = (uint32_t)rows;
+    a.cols = (uint32_t)cols;
+    if (operand) {
+        a.q = static_cast<uint8_t*>(operand);
+        a.s = a.q + o.scale_off;
+        a.pitch = o.pitch;
+        a.s_pitch = (uint32_t)o.scale_pitch;
+    }
+    if (operand_t) {
+        a.qt = static_cast<uint8_t*>(operand_t);
+        a.st = a.qt + t.scale_off;
+        a.pitch_t = t.pitch;
+        a.s_pitch_t = (uint32_t)t.scale_pitch;
+    }
+    a.tiles_c = (uint32_t)(o.pitch / DEMO_BLOCK);
+    a.wide = aligned16(src) && ld * eb % 16 == 0 && cols % 8 == 0;
+    const dim3 grid(a.tiles_c * (uint32_t)((rows + DEMO_BLOCK - 1) / DEMO_BLOCK));
+    hipStream_t s = static_cast<hipStream_t>(hip_stream);
+    switch (cfg->dtype) {
+    case DEMO_DTYPE_F32: return status_of(launch_quantize<float>(a, cfg, grid, s));
+    case DEMO_DTYPE_F16: return status_of(launch_quantize<demo::f16_t>(a, cfg, grid, s));
+    default: return status_of(launch_quantize<demo::bf16_t>(a, cfg, grid, s));
+    }
+}
+
+int demo_block_workspace(const demo_product_cfg* cfg, uint64_t m, uint64_t n, uint64_t k, uint64_t* bytes) {
+    if (const int rc = check_product(cfg, m, n, k)) return rc;
+    if (!bytes) return DEMO_EINVAL;
+    const Plan plan = plan_of(m, n, k);
+    *bytes = plan.splits > 1 ? plan.splits * m * n * 4 : 0;
+    return DEMO_OK;
+}
+
+int demo_block_matmul(const demo_product_cfg* cfg, uint64_t m, uint64_t n, uint64_t k, const void* a, const void* b,
+                      void* c, uint64_t ldc, const void* addend, uint64_t ld_addend, const demo_dropout_cfg* dropout,
+                      void* workspace, uint64_t workspace_bytes, void* hip_stream) {
+    if (const int rc = check_product(cfg, m, n, k)) return rc;
+    if (ldc < n || ldc > DEMO_MAX_ELEMS) return DEMO_EINVAL;
+    if (addend && (ld_addend < n || ld_addend > DEMO_MAX_ELEMS)) return DEMO_EINVAL;
+    demo::ProductArgs p{};
+    if (const int rc = drop_of(dropout, m * n, &p.drop)) return rc;
+    if (!a || !b || !c) return DEMO_EINVAL;
+    const uint64_t eb = elem_bytes(cfg->dtype);
+    if (!aligned16(a) || !aligned16(b) || !aligned_to(c, eb) || !aligned_to(addend, eb) || !aligned16(workspace))
+        return DEMO_EALIGN;
+    const demo_operand oa = operand_of(m, k), ob = operand_of(n, k);
+    const uint64_t cb = ((m - 1) * ldc + n) * eb, db = addend ? ((m - 1) * ld_addend + n) * eb : 0;
+    const bool in_place = addend == c && ld_addend == ldc;
+    if (overlap(c, cb, a, oa.total_bytes) || overlap(c, cb, b, ob.total_bytes) || (!in_place && overlap(c, cb, addend, db)))
+        return DEMO_EINVAL;
+    uint64_t need = 0;
+    if (const int rc = demo_block_workspace(cfg, m, n, k, &need)) return rc;
+    if (need && (!workspace || workspace_bytes < need)) return DEMO_EINVAL;
+    if (need && (overlap(workspace, need, a, oa.total_bytes) || overlap(workspace, need, b, ob.total_bytes) ||
+                 overlap(workspace, need, c, cb) || overlap(workspace, need, addend, db)))
+        return DEMO_EINVAL;
+    p.a = static_cast<const uint8_t*>(a);
+    p.b = static_cast<const uint8_t*>(b);
+    p.sa = p.a + oa.scale_off;
+    p.sb = p.b + ob.scale_off;
+    p.m = (uint32_t)m;
+    p.n = (uint32_t)n;
+    p.kb = (uint32_t)(oa.pitch / DEMO_BLOCK);
+    p.pitch = (uint32_t)oa.pitch;
+    p.s_pitch = (uint32_t)oa.scale_pitch;
+    p.c = c;
+    p.addend = addend;
+    p.ldc = ldc;
+    p.ld_addend = addend ? ld_addend : 0;
+    p.dtype = cfg->dtype;
+    p.wide_c = aligned16(c) && ldc * eb % 16 == 0;
+    p.wide_addend = aligned16(addend) && ld_addend * eb % 16 == 0;
+    const Plan plan = plan_of(m, n, k);
+    hipStream_t s = static_cast<hipStream_t>(hip_stream);
+    if (cfg->fmt_a == DEMO_FMT_E4M3)
+        return status_of(cfg->fmt_b == DEMO_FMT_E4M3 ? launch_product<demo::kE4M3, demo::kE4M3>(p, plan, workspace, s)
+                                                     : launch_product<demo::kE4M3, demo::kE5M2>(p, plan, workspace, s));
+    return status_of(cfg->fmt_b == DEMO_FMT_E4M3 ? launch_product<demo::kE5M2, demo::kE4M3>(p, plan, workspace, s)
+                                                 : launch_product<demo::kE5M2, demo::kE5M2>(p, plan, workspace, s));
+}
+
+}  // extern "C"

@@ -1,0 +1,68 @@
+// number.hpp -- the storage types of the linear-layer operators (fp32, fp16,
+// bf16, 8-bit e4m3 and e5m2) and their conversions.  Every rounding is to
+// nearest even, by the hardware's conversions.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace demo {
+
+typedef __bf16 bf16_t;
+typedef _Float16 f16_t;
+typedef float float4_v __attribute__((ext_vector_type(4)));
+typedef uint32_t uint4_v __attribute__((ext_vector_type(4)));
+typedef uint32_t uint2_v __attribute__((ext_vector_type(2)));
+
+template <typename T>
+__device__ __forceinline__ float to_float(T x) { return (float)x; }
+template <typename T>
+__device__ __forceinline__ T from_float(float x) { return (T)x; }
+
+// eight values from a 16-byte aligned address
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+    const float4_v a = *(const float4_v*)p, b = *(const float4_v*)(p + 4);
+#pragma unroll
+    for (int j = 0; j < 4; j++) v[j] = a[j], v[4 + j] = b[j];
+}
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
+    static_assert(sizeof(T) == 2, "two-byte type");
+    typedef T vec __attribute__((ext_vector_type(8)));
+    const vec a = *(const vec*)p;
+#pragma unroll
+    for (int j = 0; j < 8; j++) v[j] = (float)a[j];
+}
+
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+    *(float4_v*)p = float4_v{v[0], v[1], v[2], v[3]};
+    *(float4_v*)(p + 4) = float4_v{v[4], v[5], v[6], v[7]};
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float (&v)[8]) {
+    static_assert(sizeof(T) == 2, "two-byte type");
+    typedef T vec __attribute__((ext_vector_type(8)));
+    vec a;
+#pragma unroll
+    for (int j = 0; j < 8; j++) a[j] = (T)v[j];
+    *(vec*)p = a;
+}
+
+constexpr int kE4M3 = 0, kE5M2 = 1;
+
+// four 8-bit codes of four floats inside the format's range (NaN gives a NaN
+// code), the first in the low byte
+template <int FMT>
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
+    int w = 0;
+    if (FMT == kE4M3) {
+        w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, w, false);
+        w = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
+    } else {
+        w = __builtin_amdgcn_cvt_pk_bf8_f32(a, b, w, false);
+        w = __builtin_amdgcn_cvt_pk_bf8_f32(c, d, w, true);
+    }
+    return (uint32_t)w;
+}
+
+}  // namespace demo

@@ -1,0 +1,388 @@
+// product.hpp -- matrix product of block-scaled 8-bit operands (gfx950).
+//
+//   C[i, j] = addend[i, j] + drop( sum_b 2^(ea[i,b] + eb[j,b]) sum_{k in block b} A[i,k] B[j,k] )
+//
+// Both operands are stored along the summed axis with the pitch padded to 128
+// by zeros, so no tail of the sum needs care.  There are two ways to multiply:
+//
+//  * scaled 8-bit matrix instructions (4.75 PFLOP/s from registers): they
+//    apply both scales by themselves and accumulate in fp32, but line up the
+//    eight products of each 8 neighbouring values of the sum at the largest of
+//    them and keep 13 binary places below it.  On random data that is 1.4e-5 of the result,
+//    a hundredth of the rounding of a 16-bit result, so 16-bit results take it;
+//  * bf16 matrix instructions (2.48 PFLOP/s from registers) on codes widened
+//    to bf16 with their scale, which is exact, and whose products and sums are
+//    those of fp32: fp32 results take it (WIDE).  A code times its scale has to
+//    stay below 2^128, bf16's range.
+#pragma once
+
+#include "dropout.hpp"
+
+namespace demo {
+
+typedef int v8i __attribute__((ext_vector_type(8)));
+typedef int v4i __attribute__((ext_vector_type(4)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+
+constexpr int kBlkK = 128;  // codes per scale
+constexpr uint32_t kF32 = 0, kF16 = 1, kBF16 = 2;
+
+struct ProductArgs {
+    const uint8_t *a, *b;    // codes
+    const uint8_t *sa, *sb;  // scale bytes
+    uint32_t m, n;
+    uint32_t kb;             // blocks of 128 along the sum
+    uint32_t pitch;          // of both operands' codes
+    uint32_t s_pitch;        // of both operands' scale bytes
+    void* c;
+    const void* addend;      // NULL: none
+    uint64_t ldc, ld_addend;
+    uint32_t dtype;
+    uint32_t wide_c, wide_addend;  // eight neighbouring elements are aligned accesses of 16 bytes
+    uint32_t tiles_m, tiles_n;
+    uint32_t kb_split;  // blocks of 128 along the sum of one split, a multiple of 4
+    float* partial;     // [split][m][n] sums of more than one split, else NULL
+    Drop drop;
+};
+
+// 64 lanes' 16 bytes at base + offset into LDS at `lds` + 16 lane, in flight
+// until the next vmcnt wait
+__device__ __forceinline__ void load_lds16(const uint8_t* base, uint32_t offset, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(offset), "s"(base)
+                 : "memory", "m0");
+}
+// the same with 4 bytes a lane
+__device__ __forceinline__ void load_lds4(const uint8_t* base, uint32_t offset, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(lds), "v"(offset), "s"(base)
+                 : "memory", "m0");
+}
+
+// up to eight neighbouring elements of a row, as floats
+template <typename T>
+__device__ __forceinline__ void add_row(const T* p, int count, bool wide, float (&v)[8]) {
+    if (wide && count == 8) {
+        float w[8];
+        load8(p, w);
+#pragma unroll
+        for (int q = 0; q < 8; q++) v[q] += w[q];
+    } else {
+#pragma unroll
+        for (int q = 0; q < 8; q++)
+            if (q < count) v[q] += to_float(p[q]);
+    }
+}
+template <typename T>
+__device__ __forceinline__ void put_row(T* p, int count, bool wide, const float (&v)[8]) {
+    if (wide && count == 8) {
+        store8(p, v);
+    } else {
+#pragma unroll
+        for (int q = 0; q < 8; q++)
+            if (q < count) p[q] = from_float<T>(v[q]);
+    }
+}
+
+// C[i, j..j+7] from eight sums: drop, add, round once, store
+__device__ __forceinline__ void finish8(const ProductArgs& p, uint32_t i, uint32_t j, float (&v)[8]) {
+    if (i >= p.m || j >= p.n) return;
+    const int count = (int)min(p.n - j, 8u);
+    if (p.drop.on) {
+        const uint32_t keep = keep8(p.drop, (uint64_t)i * p.n + j);
+#pragma unroll
+        for (int q = 0; q < 8; q++) v[q] = keep >> q & 1 ? v[q] * p.drop.scale : 0.f;
+    }
+    const uint64_t at = (uint64_t)i * p.ldc + j, ad = (uint64_t)i * p.ld_addend + j;
+    if (p.dtype == kF32) {
+        if (p.addend) add_row((const float*)p.addend + ad, count, p.wide_addend, v);
+        put_row((float*)p.c + at, count, p.wide_c, v);
+    } else if (p.dtype == kF16) {
+        if (p.addend) add_row((const f16_t*)p.addend + ad, count, p.wide_addend, v);
+        put_row((f16_t*)p.c + at, count, p.wide_c, v);
+    } else {
+        if (p.addend) add_row((const bf16_t*)p.addend + ad, count, p.wide_addend, v);
+        put_row((bf16_t*)p.c + at, count, p.wide_c, v);
+    }
+}
+
+// A wave's SM x SN accumulators of 16 x 16 (lane l holds row l % 16, columns 4
+// (l / 16) .. +3 of each) go to C through a piece of LDS of the wave's own, 32
+// rows at a time: a lane then holds eight neighbours, which makes one 16-byte
+// access of a 16-bit row and one Philox block.  Four floats of padding a row
+// keep the accesses off each other's banks.
+template <int SM, int SN>
+constexpr int finish_bytes() { return 32 * (SN * 16 + 4) * 4; }
+
+template <int SM, int SN>
+__device__ __forceinline__ void finish(const ProductArgs& p, const v4f (&acc)[SM][SN], float* slab, uint32_t i0,
+                                       uint32_t j0, int lane) {
+    constexpr int kRow = SN * 16 + 4, kLanes = SN * 2, kRows = 64 / kLanes, H = SM < 2 ? 1 : 2;
+    static_assert(SM % H == 0, "whole slabs");
+#pragma unroll
+    for (int s = 0; s < SM / H; s++) {
+#pragma unroll
+        for (int i = 0; i < H; i++)
+#pragma unroll
+            for (int j = 0; j < SN; j++)
+                *(v4f*)(slab + (i * 16 + (lane & 15)) * kRow + j * 16 + 4 * (lane >> 4)) = acc[s * H + i][j];
+        wave_lds_sync();
+#pragma unroll 1
+        for (int r = lane / kLanes; r < 16 * H; r += kRows) {
+            const float* src = slab + r * kRow + lane % kLanes * 8;
+            float v[8];
+            load8(src, v);
+            finish8(p, i0 + s * 16 * H + r, j0 + lane % kLanes * 8, v);
+        }
+        wave_lds_sync();
+    }
+}
+
+typedef __bf16 v8b __attribute__((ext_vector_type(8)));
+
+// 2^(byte - 127)
+__device__ __forceinline__ float scale_float(uint32_t byte) {
+    return __uint_as_float(byte ? byte << 23 : 0x00400000u);
+}
+
+// eight codes (two words) as bf16 times their scale: exact
+template <int FMT>
+__device__ __forceinline__ v8b widen(int lo, int hi, float scale) {
+    typedef __bf16 v2b __attribute__((ext_vector_type(2)));
+    v2b w[4];
+    if (FMT == kE4M3) {
+        w[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)lo, scale, false);
+        w[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)lo, scale, true);
+        w[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)hi, scale, false);
+        w[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)hi, scale, true);
+    } else {
+        w[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8((uint32_t)lo, scale, false);
+        w[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8((uint32_t)lo, scale, true);
+        w[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8((uint32_t)hi, scale, false);
+        w[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8((uint32_t)hi, scale, true);
+    }
+    return v8b{w[0][0], w[0][1], w[1][0], w[1][1], w[2][0], w[2][1], w[3][0], w[3][1]};
+}
+
+// acc += 16 x 16 pieces of A's SM and B's SN fragments over 128 of the sum.  A
+// fragment's lane l holds 32 codes of row l % 16, those of chunks 2 (l / 16)
+// and + 1; both operands use the same order, so any order is right.  ea and eb
+// hold the rows' scale bytes in their lowest bytes.  Columns of C run along
+// the instruction's rows: a lane's four sums are neighbours in memory.
+template <int FA, int FB, bool WIDE, int SM, int SN>
+__device__ __forceinline__ void multiply(v4f (&acc)[SM][SN], const v8i (&fa)[SM], const v8i (&fb)[SN],
+                                         const uint32_t (&ea)[SM], const uint32_t (&eb)[SN]) {
+    if constexpr (WIDE) {
+        float ka[SM], kb[SN];
+#pragma unroll
+        for (int i = 0; i < SM; i++) ka[i] = scale_float(ea[i] & 255u);
+#pragma unroll
+        for (int j = 0; j < SN; j++) kb[j] = scale_float(eb[j] & 255u);
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+            v8b wb[SN];
+#pragma unroll
+            for (int j = 0; j < SN; j++) wb[j] = widen<FB>(fb[j][2 * q], fb[j][2 * q + 1], kb[j]);
+#pragma unroll
+            for (int i = 0; i < SM; i++) {
+                const v8b wa = widen<FA>(fa[i][2 * q], fa[i][2 * q + 1], ka[i]);
+#pragma unroll
+                for (int j = 0; j < SN; j++)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j], wa, acc[i][j], 0, 0, 0);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < SM; i++)
+#pragma unroll
+            for (int j = 0; j < SN; j++)
+                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[j], fa[i], acc[i][j], FB, FA, 0,
+                                                                             (int)eb[j], 0, (int)ea[i]);
+    }
+}
+
+// Where this workgroup's sums go: the result, or its split's plane of the partial sums.
+__device__ __forceinline__ ProductArgs target(const ProductArgs& p, uint32_t split) {
+    ProductArgs t = p;
+    if (p.partial) {
+        t.c = p.partial + (uint64_t)split * p.m * p.n;
+        t.ldc = p.n;
+        t.dtype = kF32;
+        t.addend = nullptr;
+        t.wide_c = p.n % 4 == 0;
+        t.drop.on = 0;
+    }
+    return t;
+}
+
+// Tile of workgroup `id`: the 8 XCDs, which take ids in turn, get runs of
+// neighbouring tiles each, and a run goes down kTileRun row tiles before it
+// takes the next column tile, so that one XCD's workgroups share rows of both
+// operands in its L2.
+constexpr uint32_t kTileRun = 8;
+
+__device__ __forceinline__ void tile_of(const ProductArgs& p, uint32_t id, uint32_t& tm, uint32_t& tn) {
+    const uint32_t tiles = p.tiles_m * p.tiles_n, q = tiles / kXcds, r = tiles % kXcds, x = id % kXcds;
+    id = x * q + min(x, r) + id / kXcds;
+    const uint32_t band = kTileRun * p.tiles_n, first = id / band * kTileRun, high = min(p.tiles_m - first, kTileRun);
+    tm = first + id % band % high;
+    tn = id % band / high;
+}
+
+// BM x BN of C by WM x WN waves, one of the splits of the sum (grid y).  LDS
+// holds two stages of 128 along the sum, filled by loads that go from memory to
+// LDS; one barrier a stage.  Row r's 16-byte chunk c sits at c ^ (r / 2 & 7),
+// which spreads 16 rows' reads of one chunk over all 64 banks; loads into LDS
+// write lanes in order, so the exchange is made on their source addresses.
+// Rows past the matrix repeat its last row; what they give is not stored.
+template <int FA, int FB, bool WIDE, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN) void product_kernel(ProductArgs p) {
+    constexpr int NW = WM * WN, SM = BM / WM / 16, SN = BN / WN / 16;
+    constexpr int LA = BM / 8 / NW, LB = BN / 8 / NW;
+    constexpr int kStage = (BM + BN) * kBlkK, kScales = (BM + BN) * 4;
+    static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0 && BM % 64 == 0 && (BM + BN) / 64 <= NW, "loads per wave");
+    static_assert(NW * finish_bytes<SM, SN>() <= 2 * kStage, "the way out fits the stages");
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    const uint8_t* scales = lds + 2 * kStage;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    uint32_t tm, tn;
+    tile_of(p, blockIdx.x, tm, tn);
+    const uint32_t m0 = tm * BM, n0 = tn * BN;
+    const uint32_t kb0 = blockIdx.y * p.kb_split, kb1 = min(kb0 + p.kb_split, p.kb);
+    const uint32_t lds0 = __builtin_amdgcn_readfirstlane(
+        (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds);
+
+    // this lane's place in the loads: row 8 (wave + i NW) + lane / 8
+    const uint8_t* ga = p.a + (uint64_t)m0 * p.pitch;
+    const uint8_t* gb = p.b + (uint64_t)n0 * p.pitch;
+    uint32_t oa[LA], ob[LB];
+#pragma unroll
+    for (int i = 0; i < LA; i++) {
+        const uint32_t r = 8 * (wave + i * NW) + (lane >> 3);
+        oa[i] = min(r, p.m - 1 - m0) * p.pitch + ((lane & 7) ^ (r >> 1 & 7)) * 16;
+    }
+#pragma unroll
+    for (int i = 0; i < LB; i++) {
+        const uint32_t r = 8 * (wave + i * NW) + (lane >> 3);
+        ob[i] = min(r, p.n - 1 - n0) * p.pitch + ((lane & 7) ^ (r >> 1 & 7)) * 16;
+    }
+    const bool scale_of_a = wave * 64 < BM;
+    const uint32_t srow = scale_of_a ? min((uint32_t)(wave * 64 + lane), p.m - 1 - m0)
+                                     : min((uint32_t)(wave * 64 - BM + lane), p.n - 1 - n0);
+    const uint8_t* gs = scale_of_a ? p.sa + (uint64_t)m0 * p.s_pitch : p.sb + (uint64_t)n0 * p.s_pitch;
+    const uint32_t os = srow * p.s_pitch;
+
+    auto fetch = [&](uint32_t kb) {
+        const uint32_t at = lds0 + (kb & 1) * kStage;
+#pragma unroll
+        for (int i = 0; i < LA; i++) load_lds16(ga + kb * kBlkK, oa[i], at + (wave + i * NW) * 1024);
+#pragma unroll
+        for (int i = 0; i < LB; i++) load_lds16(gb + kb * kBlkK, ob[i], at + BM * kBlkK + (wave + i * NW) * 1024);
+        if ((kb & 3) == 0 && wave < (BM + BN) / 64)  // four blocks' scale bytes
+            load_lds4(gs + kb, os, lds0 + 2 * kStage + (kb >> 2 & 1) * kScales + wave * 256);
+    };
+
+    const int wm = wave % WM, wn = wave / WM, row = lane & 15, g = lane >> 4;
+    const int c0 = ((2 * g) ^ (row >> 1)) * 16, c1 = ((2 * g + 1) ^ (row >> 1)) * 16;
+    v4f acc[SM][SN] = {};
+    uint32_t ea[SM], eb[SN];
+    fetch(kb0);
+    for (uint32_t kb = kb0; kb < kb1; kb++) {
+        // this wave's loads have landed, then everyone's; and everyone has
+        // read the stage that is filled next
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        if (kb + 1 < kb1) fetch(kb + 1);
+        if ((kb & 3) == 0) {
+            const uint32_t* sc = (const uint32_t*)(scales + (kb >> 2 & 1) * kScales);
+#pragma unroll
+            for (int i = 0; i < SM; i++) ea[i] = sc[(wm * SM + i) * 16 + row];
+#pragma unroll
+            for (int i = 0; i < SN; i++) eb[i] = sc[BM + (wn * SN + i) * 16 + row];
+        }
+        const uint8_t* sa = lds + (kb & 1) * kStage + (wm * SM * 16 + row) * kBlkK;
+        const uint8_t* sb = lds + (kb & 1) * kStage + (BM + wn * SN * 16 + row) * kBlkK;
+        v8i fa[SM], fb[SN];
+#pragma unroll
+        for (int i = 0; i < SN; i++)
+            fb[i] = __builtin_shufflevector(*(const v4i*)(sb + i * 16 * kBlkK + c0),
+                                            *(const v4i*)(sb + i * 16 * kBlkK + c1), 0, 1, 2, 3, 4, 5, 6, 7);
+#pragma unroll
+        for (int i = 0; i < SM; i++)
+            fa[i] = __builtin_shufflevector(*(const v4i*)(sa + i * 16 * kBlkK + c0),
+                                            *(const v4i*)(sa + i * 16 * kBlkK + c1), 0, 1, 2, 3, 4, 5, 6, 7);
+        multiply<FA, FB, WIDE>(acc, fa, fb, ea, eb);
+#pragma unroll
+        for (int i = 0; i < SM; i++) ea[i] >>= 8;
+#pragma unroll
+        for (int i = 0; i < SN; i++) eb[i] >>= 8;
+    }
+    __syncthreads();
+    finish<SM, SN>(target(p, blockIdx.y), acc, (float*)(lds + wave * finish_bytes<SM, SN>()), m0 + wm * SM * 16,
+                   n0 + wn * SN * 16, lane);
+}
+
+// 32 codes from a 16-byte aligned address
+__device__ __forceinline__ v8i load_codes(const uint8_t* p) {
+    return __builtin_shufflevector(*(const v4i*)p, *(const v4i*)(p + 16), 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// Few rows: 16 columns of C for up to 16 SM rows by NW waves that share the
+// sum among them, each taking every NW-th block of 128 straight from memory
+// (nothing is used twice), and add up in LDS in the order of the waves.
+template <int FA, int FB, bool WIDE, int SM, int NW>
+__global__ __launch_bounds__(64 * NW) void product_few_kernel(ProductArgs p) {
+    __shared__ __attribute__((aligned(16))) float sums[NW][SM][16 * 20];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, row = lane & 15, g = lane >> 4;
+    const uint32_t n0 = blockIdx.x * 16;
+    const uint32_t rb = min(n0 + row, p.n - 1);
+    const uint8_t* qb = p.b + (uint64_t)rb * p.pitch + g * 32;
+    const uint8_t* xb = p.sb + (uint64_t)rb * p.s_pitch;
+    const uint8_t *qa[SM], *xa[SM];
+#pragma unroll
+    for (int i = 0; i < SM; i++) {
+        const uint32_t ra = min((uint32_t)(i * 16 + row), p.m - 1);
+        qa[i] = p.a + (uint64_t)ra * p.pitch + g * 32;
+        xa[i] = p.sa + (uint64_t)ra * p.s_pitch;
+    }
+    v4f acc[SM][1] = {};
+#pragma unroll 4
+    for (uint32_t kb = wave; kb < p.kb; kb += NW) {
+        v8i fa[SM], fb[1];
+        uint32_t ea[SM], eb[1] = {xb[kb]};
+        fb[0] = load_codes(qb + kb * kBlkK);
+#pragma unroll
+        for (int i = 0; i < SM; i++) {
+            fa[i] = load_codes(qa[i] + kb * kBlkK);
+            ea[i] = xa[i][kb];
+        }
+        multiply<FA, FB, WIDE>(acc, fa, fb, ea, eb);
+    }
+#pragma unroll
+    for (int i = 0; i < SM; i++) *(v4f*)&sums[wave][i][row * 20 + 4 * g] = acc[i][0];
+    __syncthreads();
+    // two lanes a row, eight columns each
+    for (uint32_t t = threadIdx.x; t < SM * 32; t += 64 * NW) {
+        const uint32_t r = t >> 1, c = (t & 1) * 8;
+        float v[8] = {};
+        for (int w = 0; w < NW; w++) {
+            const float* s = &sums[w][r >> 4][(r & 15) * 20 + c];
+#pragma unroll
+            for (int q = 0; q < 8; q++) v[q] += s[q];
+        }
+        finish8(p, r, n0 + c, v);
+    }
+}
+
+// The splits' partial sums, added in their order, to the result.
+__global__ __launch_bounds__(256) void product_join_kernel(ProductArgs p, uint32_t splits) {
+    const uint32_t groups = (p.n + 7) / 8;
+    const uint64_t total = (uint64_t)p.m * groups, plane = (uint64_t)p.m * p.n;
+    for (uint64_t t = (uint64_t)blockIdx.x * 256 + threadIdx.x; t < total; t += (uint64_t)gridDim.x * 256) {
+        const uint32_t i = (uint32_t)(t / groups), j = (uint32_t)(t % groups) * 8;
+        const float* s = p.partial + (uint64_t)i * p.n + j;
+        const int count = (int)min(p.n - j, 8u);
+        float v[8] = {};
+        for (uint32_t z = 0; z < splits; z++) add_row(s + z * plane, count, p.n % 4 == 0, v);
+        finish8(p, i, j, v);
+    }
+}
+
+}  // namespace demo

@@ -233,6 +233,127 @@ int demo_payload_validate(const demo_cfg *cfg, uint64_t n_elems, const void *pay
 int demo_random_select(const demo_cfg *cfg, uint64_t seed, uint64_t step, uint64_t n_chunks,
                        uint32_t *masks_out, void *hip_stream);
 
+/*
+ * The low-precision linear layer beside the optimizer step: a layer whose fp32
+ * master weight is a piece of the shard, whose products run on 8-bit operands
+ * with a scale for each block of 128 along the sum, and whose weight gradient
+ * is added in fp32 to the gradient that demo_encode reads.
+ *
+ * Types of matrices that are not operands.
+ */
+enum { DEMO_DTYPE_F32 = 0, DEMO_DTYPE_F16 = 1, DEMO_DTYPE_BF16 = 2 };
+
+/* 8-bit formats (OCP): e4m3 reaches 448 and has no infinity, e5m2 reaches
+ * 57344. */
+enum { DEMO_FMT_E4M3 = 0, DEMO_FMT_E5M2 = 1 };
+
+#define DEMO_BLOCK 128
+#define DEMO_BLOCK_MAX_K ((uint64_t)1 << 22) /* longest sum of a product */
+#define DEMO_BLOCK_MAX_WORKSPACE ((uint64_t)64 << 20) /* no product needs more */
+
+/*
+ * Dropout from a counter: element e = 32*chunk_offset + i takes the 16-bit
+ * half e % 2 of word (e % 8)/2 of Philox4x32-10 with key `seed` and counter
+ * (e/8 mod 2^32, e/8 div 2^32, step mod 2^32, 2*2^24 + site), and is kept iff
+ * that number is at least T = floor(65536 p + 1/2); kept values are scaled by
+ * 65536/(65536 - T) in fp32 (0 for T = 65536).  A shard that starts at
+ * chunk_offset draws what the whole tensor draws there, and no draw of
+ * demo_random_select with the same seed coincides with one of these.
+ */
+typedef struct demo_dropout_cfg {
+    uint32_t abi_version;  /* must be DEMO_ABI_VERSION */
+    float p;               /* probability of dropping, in [0, 1], taken to the nearest multiple of 2^-16 */
+    uint32_t site;         /* which dropout of the model, below 2^24 */
+    uint32_t reserved;     /* must be 0 */
+    uint64_t seed;
+    uint64_t step;
+    uint64_t chunk_offset; /* global chunk index of element 0 */
+} demo_dropout_cfg;
+
+/*
+ * An operand of the product: `rows` rows of codes with a pitch of the next
+ * multiple of 128 bytes (codes behind the last column are 0), then at
+ * scale_off one byte e + 127 for each row and block of 128 columns, with a
+ * pitch of the next multiple of 4 bytes.  A code c of that block stands for
+ * c * 2^e.  Operands are 16-byte aligned.
+ */
+typedef struct demo_operand {
+    uint64_t pitch;
+    uint64_t scale_off;
+    uint64_t scale_pitch;
+    uint64_t total_bytes;
+} demo_operand;
+
+typedef struct demo_block_cfg {
+    uint32_t abi_version;
+    uint32_t fmt;   /* DEMO_FMT_* of the codes */
+    uint32_t tile;  /* 0: a scale for 128 values of a row; 1: for a square of 128 x 128 */
+    uint32_t dtype; /* DEMO_DTYPE_* of src */
+} demo_block_cfg;
+
+typedef struct demo_product_cfg {
+    uint32_t abi_version;
+    uint32_t fmt_a, fmt_b; /* DEMO_FMT_* of the operands */
+    uint32_t dtype;        /* DEMO_DTYPE_* of c and addend */
+} demo_product_cfg;
+
+/*
+ * y = residual + (kept ? x*scale : 0), in fp32 and rounded once to the
+ * tensors' common type; residual may be NULL.  1 <= n_elems <= DEMO_MAX_ELEMS;
+ * 16-byte aligned.  y may be x or residual themselves, else it overlaps
+ * neither.  A dropped NaN or infinity leaves nothing.
+ */
+int demo_dropout(const demo_dropout_cfg *cfg, uint32_t dtype, uint64_t n_elems, const void *x, const void *residual,
+                 void *y, void *hip_stream);
+
+/*
+ * The gradient of demo_dropout for x under the same cfg: dx = kept ? dy*scale
+ * : 0, the mask drawn again (the residual's gradient is dy itself).  dx may be
+ * dy.
+ */
+int demo_dropout_backward(const demo_dropout_cfg *cfg, uint32_t dtype, uint64_t n_elems, const void *dy, void *dx,
+                          void *hip_stream);
+
+/* Layout of an operand of rows x cols (cols is the summed axis); host-only.
+ * Both sides at most 2^30, their product at most DEMO_MAX_ELEMS. */
+int demo_block_layout(uint64_t rows, uint64_t cols, demo_operand *out);
+
+/*
+ * Quantises src [rows][cols] (row pitch ld elements, aligned to its element)
+ * into operand (rows x cols, blocks along the columns) and into operand_t
+ * (cols x rows: the transposed matrix, blocks along the rows) in one pass;
+ * one of the two may be NULL.  A block's scale is 2^e with the smallest e >=
+ * -127 that keeps its largest finite magnitude within the format; codes are
+ * rounded to nearest even; infinities and NaN become NaN codes.  With dropout
+ * the values are first multiplied as demo_dropout_backward does (element i =
+ * row*cols + column), in fp32 without a rounding between.
+ */
+int demo_block_quantize(const demo_block_cfg *cfg, uint64_t rows, uint64_t cols, const void *src, uint64_t ld,
+                        const demo_dropout_cfg *dropout, void *operand, void *operand_t, void *hip_stream);
+
+/* Bytes of workspace demo_block_matmul needs for these sizes (0 for most, at
+ * most DEMO_BLOCK_MAX_WORKSPACE); host-only. */
+int demo_block_workspace(const demo_product_cfg *cfg, uint64_t m, uint64_t n, uint64_t k, uint64_t *bytes);
+
+/*
+ * c[i][j] = addend[i][j] + drop(sum over k of a[i][k]*b[j][k]) for operands a
+ * (m x k) and b (n x k): with X, W and dY the matrices of a layer Y = X W^T,
+ *   Y  = product of X's operand and W's,
+ *   dX = product of dY's operand and W's operand_t,
+ *   dW = product of dY's operand_t and X's operand_t.
+ * Sums are held in fp32 and the result is rounded once; the order of the sums
+ * depends on the sizes only.  addend may be NULL, or c itself with the same
+ * pitch (to add to a gradient); dropout (NULL: none) applies to the product as
+ * demo_dropout does, element i*n + j.  c and addend [m][n] with row pitches
+ * ldc and ld_addend in elements, aligned to their element.  m, n at most 2^30,
+ * k at most DEMO_BLOCK_MAX_K (DEMO_EUNSUPPORTED beyond).  The workspace is
+ * written by the call and free again when it has run: calls that may run at
+ * the same time (other streams, other graphs) need one each.
+ */
+int demo_block_matmul(const demo_product_cfg *cfg, uint64_t m, uint64_t n, uint64_t k, const void *a, const void *b,
+                      void *c, uint64_t ldc, const void *addend, uint64_t ld_addend,
+                      const demo_dropout_cfg *dropout, void *workspace, uint64_t workspace_bytes, void *hip_stream);
+
 #ifdef __cplusplus
 }
 #endif
