@@ -7,7 +7,7 @@
 
 #include "demo.h"
 #include "host.hpp"
-#include "product.hpp"
+#include "product_big.hpp"
 #include "quantize.hpp"
 
 namespace {
@@ -108,7 +108,6 @@ int check_product(const demo_product_cfg* cfg, uint64_t m, uint64_t n, uint64_t 
     return DEMO_OK;
 }
 
-constexpr uint64_t kCus = 256;
 constexpr uint64_t kFewRows = 64;
 
 // How a product is cut: tiles of `tile` x `tile` and `splits` of the sum, or
@@ -119,22 +118,42 @@ struct Plan {
     uint32_t kb_split;
 };
 
-Plan plan_of(uint64_t m, uint64_t n, uint64_t k) {
+// The card runs 256 tiles of 256 x 256 at a time, or 512 of 128 x 128 or 64 x
+// 64 (two workgroups a CU).  Measured, 16-bit result:
+//  * a round of 256 tiles costs 1.6 to 1.8 rounds of 128 tiles (8192 x 2048 x
+//    2048: 32.2 against 38.3 us; 6144 x 4096 x 2048, where the second round is
+//    half empty: 56.3 against 53.9 us; 4096 x 2048 x 2048, half a round: 25.6
+//    against 19.9 us), so they are taken where rounds say so at 1.65;
+//  * up to 192 tiles of 128, tiles of 64 fill the card better (1024 x 2048 x
+//    2048: 9.8 against 15.6 us; 2048 x 2048 x 2048, 256 tiles: 17.0 against 15.8);
+//  * the sum is split where tiles fill less than a round: down to 16 blocks of
+//    128 for tiles of 64 (256 x 2048 x 8192: 17.4 us in 4, 24.0 in one; 128 x
+//    2048 x 2048: 8.1 us in one, 10.7 in 2), to 64 for tiles of 128 (2048 x 2048
+//    x 16384: 80 us in 2, 90 in one).
+// fp32 results behave the same without the tiles of 256: what bounds them is
+// the bf16 instructions' power, not reading LDS (8192 x 8192 x 8192 at 1.24
+// PFLOP/s in tiles of 128, 1.26 in tiles of 256).
+Plan plan_of(uint64_t m, uint64_t n, uint64_t k, bool wide) {
     const uint64_t kb = up(k, DEMO_BLOCK) / DEMO_BLOCK;
     if (m <= kFewRows) return {0, 1, (uint32_t)kb};
     const auto tiles = [&](uint64_t t) { return up(m, t) / t * (up(n, t) / t); };
-    if (tiles(256) >= 3 * kCus) return {256, 1, (uint32_t)up(kb, 4)};
-    uint64_t splits = 1;
-    const uint64_t t = tiles(128);
-    if (t <= kCus) {
-        splits = 2 * kCus / t;
-        const uint64_t most = (kb + 7) / 8;  // at least 8 blocks of 128 each
-        if (splits > most) splits = most;
-        while (splits > 1 && splits * m * n * 4 > DEMO_BLOCK_MAX_WORKSPACE) splits--;
-        if (splits < 1) splits = 1;
-    }
+    const auto rounds = [](uint64_t count, uint64_t at_once) { return (count + at_once - 1) / at_once; };
+    if (!wide && m >= 256 && n >= 256 && 33 * rounds(tiles(256), 256) <= 20 * rounds(tiles(128), 512))
+        return {256, 1, (uint32_t)up(kb, 4)};
+    const uint64_t tile = tiles(128) > 192 ? 128 : 64, least = tile == 128 ? 64 : 16;
+    uint64_t splits = 512 / tiles(tile);
+    if (splits > kb / least) splits = kb / least;
+    if (splits < 1) splits = 1;
     const uint64_t each = up((kb + splits - 1) / splits, 4);
-    return {128, (uint32_t)((kb + each - 1) / each), (uint32_t)each};
+    return {(uint32_t)tile, (uint32_t)((kb + each - 1) / each), (uint32_t)each};
+}
+// the partial sums of up to 512 tiles of 128 x 128
+static_assert(512 * 128 * 128 * 4 <= DEMO_BLOCK_MAX_WORKSPACE, "workspace");
+
+template <int FA, int FB, bool WIDE, int TILE, int STAGES>
+hipError_t launch_tiles(const demo::ProductArgs& a, dim3 grid, hipStream_t s) {
+    return launch(demo::product_kernel<FA, FB, WIDE, TILE, TILE, 2, 2, STAGES>, grid, dim3(256),
+                  STAGES * 2 * TILE * DEMO_BLOCK + 2 * 2 * TILE * 4, s, a);
 }
 
 template <int FA, int FB, bool WIDE>
@@ -151,10 +170,10 @@ hipError_t launch_product(demo::ProductArgs a, const Plan& plan, void* workspace
     a.tiles_m = (a.m + plan.tile - 1) / plan.tile;
     a.tiles_n = (a.n + plan.tile - 1) / plan.tile;
     const dim3 grid(a.tiles_m * a.tiles_n, plan.splits);
-    const size_t lds = 2 * (2 * plan.tile) * (DEMO_BLOCK + 4);
-    hipError_t e = plan.tile == 256
-                       ? launch(demo::product_kernel<FA, FB, WIDE, 256, 256, 2, 4>, grid, dim3(512), lds, s, a)
-                       : launch(demo::product_kernel<FA, FB, WIDE, 128, 128, 2, 2>, grid, dim3(256), lds, s, a);
+    hipError_t e;
+    if (plan.tile == 64) e = launch_tiles<FA, FB, WIDE, 64, 4>(a, grid, s);
+    else if (WIDE || plan.tile == 128) e = launch_tiles<FA, FB, WIDE, 128, 2>(a, grid, s);
+    else e = launch(demo::product_big_kernel<FA, FB>, grid, dim3(256), demo::kBigLds, s, a);
     if (e != hipSuccess || plan.splits == 1) return e;
     const uint64_t blocks = ((uint64_t)a.m * ((a.n + 7) / 8) + 255) / 256;
     return launch(demo::product_join_kernel, dim3((unsigned)(blocks < (1u << 20) ? blocks : (1u << 20))), dim3(256), 0, s,
@@ -233,7 +252,7 @@ int demo_block_quantize(const demo_block_cfg* cfg, uint64_t rows, uint64_t cols,
 int demo_block_workspace(const demo_product_cfg* cfg, uint64_t m, uint64_t n, uint64_t k, uint64_t* bytes) {
     if (const int rc = check_product(cfg, m, n, k)) return rc;
     if (!bytes) return DEMO_EINVAL;
-    const Plan plan = plan_of(m, n, k);
+    const Plan plan = plan_of(m, n, k, cfg->dtype == DEMO_DTYPE_F32);
     *bytes = plan.splits > 1 ? plan.splits * m * n * 4 : 0;
     return DEMO_OK;
 }
@@ -275,9 +294,8 @@ int demo_block_matmul(const demo_product_cfg* cfg, uint64_t m, uint64_t n, uint6
     p.ldc = ldc;
     p.ld_addend = addend ? ld_addend : 0;
     p.dtype = cfg->dtype;
-    p.wide_c = aligned16(c) && ldc * eb % 16 == 0;
-    p.wide_addend = aligned16(addend) && ld_addend * eb % 16 == 0;
-    const Plan plan = plan_of(m, n, k);
+    p.wide = n % 8 == 0 && aligned16(c) && ldc * eb % 16 == 0 && aligned16(addend) && p.ld_addend * eb % 16 == 0;
+    const Plan plan = plan_of(m, n, k, cfg->dtype == DEMO_DTYPE_F32);
     hipStream_t s = static_cast<hipStream_t>(hip_stream);
     if (cfg->fmt_a == DEMO_FMT_E4M3)
         return status_of(cfg->fmt_b == DEMO_FMT_E4M3 ? launch_product<demo::kE4M3, demo::kE4M3>(p, plan, workspace, s)

@@ -48,6 +48,21 @@ __device__ __forceinline__ void store8(T* p, const float (&v)[8]) {
     *(vec*)p = a;
 }
 
+// store8 past the caches
+__device__ __forceinline__ void stream8(float* p, const float (&v)[8]) {
+    __builtin_nontemporal_store(float4_v{v[0], v[1], v[2], v[3]}, (float4_v*)p);
+    __builtin_nontemporal_store(float4_v{v[4], v[5], v[6], v[7]}, (float4_v*)(p + 4));
+}
+template <typename T>
+__device__ __forceinline__ void stream8(T* p, const float (&v)[8]) {
+    static_assert(sizeof(T) == 2, "two-byte type");
+    typedef T vec __attribute__((ext_vector_type(8)));
+    vec a;
+#pragma unroll
+    for (int j = 0; j < 8; j++) a[j] = (T)v[j];
+    __builtin_nontemporal_store(a, (vec*)p);
+}
+
 constexpr int kE4M3 = 0, kE5M2 = 1;
 
 // four 8-bit codes of four floats inside the format's range (NaN gives a NaN

@@ -38,7 +38,7 @@ struct ProductArgs {
     const void* addend;      // NULL: none
     uint64_t ldc, ld_addend;
     uint32_t dtype;
-    uint32_t wide_c, wide_addend;  // eight neighbouring elements are aligned accesses of 16 bytes
+    uint32_t wide;  // n is a multiple of 8, and eight neighbours of c and addend are aligned accesses of 16 bytes
     uint32_t tiles_m, tiles_n;
     uint32_t kb_split;  // blocks of 128 along the sum of one split, a multiple of 4
     float* partial;     // [split][m][n] sums of more than one split, else NULL
@@ -57,33 +57,28 @@ __device__ __forceinline__ void load_lds4(const uint8_t* base, uint32_t offset, 
                  : "memory", "m0");
 }
 
-// up to eight neighbouring elements of a row, as floats
+// C[i, j+from..j+7] from eight sums: drop, add, round once, store, element by
+// element or (wide, from 0, eight left) in aligned accesses
 template <typename T>
-__device__ __forceinline__ void add_row(const T* p, int count, bool wide, float (&v)[8]) {
-    if (wide && count == 8) {
-        float w[8];
-        load8(p, w);
+__device__ __forceinline__ void put_row(const ProductArgs& p, uint32_t i, uint32_t j, int from, int count, float (&v)[8]) {
+    T* c = (T*)p.c + (uint64_t)i * p.ldc + j;
+    const T* add = (const T*)p.addend + (p.addend ? (uint64_t)i * p.ld_addend + j : 0);
+    if (p.wide) {
+        if (p.addend) {
+            float w[8];
+            load8(add, w);
 #pragma unroll
-        for (int q = 0; q < 8; q++) v[q] += w[q];
-    } else {
-#pragma unroll
-        for (int q = 0; q < 8; q++)
-            if (q < count) v[q] += to_float(p[q]);
+            for (int q = 0; q < 8; q++) v[q] += w[q];
+        }
+        store8(c, v);
+        return;
     }
-}
-template <typename T>
-__device__ __forceinline__ void put_row(T* p, int count, bool wide, const float (&v)[8]) {
-    if (wide && count == 8) {
-        store8(p, v);
-    } else {
 #pragma unroll
-        for (int q = 0; q < 8; q++)
-            if (q < count) p[q] = from_float<T>(v[q]);
-    }
+    for (int q = 0; q < 8; q++)
+        if (q >= from && q < count) c[q] = from_float<T>((p.addend ? to_float(add[q]) : 0.f) + v[q]);
 }
 
-// C[i, j..j+7] from eight sums: drop, add, round once, store
-__device__ __forceinline__ void finish8(const ProductArgs& p, uint32_t i, uint32_t j, float (&v)[8]) {
+__device__ __forceinline__ void finish8(const ProductArgs& p, uint32_t i, uint32_t j, int from, float (&v)[8]) {
     if (i >= p.m || j >= p.n) return;
     const int count = (int)min(p.n - j, 8u);
     if (p.drop.on) {
@@ -91,46 +86,99 @@ __device__ __forceinline__ void finish8(const ProductArgs& p, uint32_t i, uint32
 #pragma unroll
         for (int q = 0; q < 8; q++) v[q] = keep >> q & 1 ? v[q] * p.drop.scale : 0.f;
     }
-    const uint64_t at = (uint64_t)i * p.ldc + j, ad = (uint64_t)i * p.ld_addend + j;
-    if (p.dtype == kF32) {
-        if (p.addend) add_row((const float*)p.addend + ad, count, p.wide_addend, v);
-        put_row((float*)p.c + at, count, p.wide_c, v);
-    } else if (p.dtype == kF16) {
-        if (p.addend) add_row((const f16_t*)p.addend + ad, count, p.wide_addend, v);
-        put_row((f16_t*)p.c + at, count, p.wide_c, v);
-    } else {
-        if (p.addend) add_row((const bf16_t*)p.addend + ad, count, p.wide_addend, v);
-        put_row((bf16_t*)p.c + at, count, p.wide_c, v);
+    if (p.dtype == kF32) put_row<float>(p, i, j, from, count, v);
+    else if (p.dtype == kF16) put_row<f16_t>(p, i, j, from, count, v);
+    else put_row<bf16_t>(p, i, j, from, count, v);
+}
+
+// eight raw neighbours of a row
+template <typename T>
+struct Row8 {
+    typedef T vec __attribute__((ext_vector_type(8)));
+};
+
+// The same for P rows at once, in aligned accesses: every load of the addend
+// is in flight before the first sum, every store behind the last.  on[r]: the
+// row and its eight columns are this tile's to write.
+template <typename T, int P>
+__device__ __forceinline__ void finish_rows(const ProductArgs& p, const uint64_t (&i)[P], uint32_t j, const bool (&on)[P],
+                                            float (&v)[P][8]) {
+    typedef typename Row8<T>::vec vec;
+    if (p.addend) {
+        vec w[P];
+#pragma unroll
+        for (int r = 0; r < P; r++)
+            if (on[r]) w[r] = *(const vec*)((const T*)p.addend + i[r] * p.ld_addend + j);
+#pragma unroll
+        for (int r = 0; r < P; r++)
+            if (on[r]) {
+#pragma unroll
+                for (int q = 0; q < 8; q++) v[r][q] += (float)w[r][q];
+            }
     }
+#pragma unroll
+    for (int r = 0; r < P; r++)
+        if (on[r]) stream8((T*)p.c + i[r] * p.ldc + j, v[r]);
 }
 
 // A wave's SM x SN accumulators of 16 x 16 (lane l holds row l % 16, columns 4
 // (l / 16) .. +3 of each) go to C through a piece of LDS of the wave's own, 32
 // rows at a time: a lane then holds eight neighbours, which makes one 16-byte
 // access of a 16-bit row and one Philox block.  Four floats of padding a row
-// keep the accesses off each other's banks.
+// keep the accesses off each other's banks.  Rows below lo_i and columns below
+// lo_j are another tile's.
 template <int SM, int SN>
-constexpr int finish_bytes() { return 32 * (SN * 16 + 4) * 4; }
+constexpr int finish_bytes() { return 16 * (SM < 2 ? 1 : 2) * (SN * 16 + 4) * 4; }
 
 template <int SM, int SN>
 __device__ __forceinline__ void finish(const ProductArgs& p, const v4f (&acc)[SM][SN], float* slab, uint32_t i0,
-                                       uint32_t j0, int lane) {
-    constexpr int kRow = SN * 16 + 4, kLanes = SN * 2, kRows = 64 / kLanes, H = SM < 2 ? 1 : 2;
-    static_assert(SM % H == 0, "whole slabs");
-#pragma unroll
-    for (int s = 0; s < SM / H; s++) {
-#pragma unroll
-        for (int i = 0; i < H; i++)
-#pragma unroll
-            for (int j = 0; j < SN; j++)
-                *(v4f*)(slab + (i * 16 + (lane & 15)) * kRow + j * 16 + 4 * (lane >> 4)) = acc[s * H + i][j];
-        wave_lds_sync();
+                                       uint32_t j0, uint32_t lo_i, uint32_t lo_j, int lane) {
+    constexpr int H = SM < 2 ? 1 : 2, kRow = SN * 16 + 4, kLanes = SN * 2, kRows = 64 / kLanes, P = 16 * H / kRows;
+    static_assert(SM % H == 0 && P >= 1, "whole slabs");
+    const uint32_t j = j0 + lane % kLanes * 8;
+    const bool col = j >= lo_j && j < p.n;
 #pragma unroll 1
-        for (int r = lane / kLanes; r < 16 * H; r += kRows) {
-            const float* src = slab + r * kRow + lane % kLanes * 8;
-            float v[8];
-            load8(src, v);
-            finish8(p, i0 + s * 16 * H + r, j0 + lane % kLanes * 8, v);
+    for (int s = 0; s < SM / H; s++) {
+        // registers have no index: one branch a slab (uniform)
+#pragma unroll
+        for (int t = 0; t < SM / H; t++)
+            if (s == t) {
+#pragma unroll
+                for (int i = 0; i < H; i++)
+#pragma unroll
+                    for (int c = 0; c < SN; c++)
+                        *(v4f*)(slab + (i * 16 + (lane & 15)) * kRow + c * 16 + 4 * (lane >> 4)) = acc[t * H + i][c];
+            }
+        wave_lds_sync();
+        const uint32_t top = i0 + s * 16 * H;
+        if (p.wide) {
+            float v[P][8];
+            uint64_t i[P];
+            bool on[P];
+#pragma unroll
+            for (int r = 0; r < P; r++) {
+                i[r] = top + r * kRows + lane / kLanes;
+                on[r] = col && i[r] >= lo_i && i[r] < p.m;
+                load8(slab + (r * kRows + lane / kLanes) * kRow + lane % kLanes * 8, v[r]);
+            }
+            if (p.drop.on) {
+#pragma unroll
+                for (int r = 0; r < P; r++) {
+                    const uint32_t keep = keep_block(p.drop, p.drop.first + ((i[r] * p.n + j) >> 3));
+#pragma unroll
+                    for (int q = 0; q < 8; q++) v[r][q] = keep >> q & 1 ? v[r][q] * p.drop.scale : 0.f;
+                }
+            }
+            if (p.dtype == kF32) finish_rows<float, P>(p, i, j, on, v);
+            else if (p.dtype == kF16) finish_rows<f16_t, P>(p, i, j, on, v);
+            else finish_rows<bf16_t, P>(p, i, j, on, v);
+        } else {
+#pragma unroll 1
+            for (int r = lane / kLanes; r < 16 * H; r += kRows) {
+                float v[8];
+                load8(slab + r * kRow + lane % kLanes * 8, v);
+                if (top + r >= lo_i) finish8(p, top + r, j, max(lo_j, j) - j, v);
+            }
         }
         wave_lds_sync();
     }
@@ -207,7 +255,7 @@ __device__ __forceinline__ ProductArgs target(const ProductArgs& p, uint32_t spl
         t.ldc = p.n;
         t.dtype = kF32;
         t.addend = nullptr;
-        t.wide_c = p.n % 4 == 0;
+        t.wide = p.n % 8 == 0;
         t.drop.on = 0;
     }
     return t;
@@ -227,21 +275,30 @@ __device__ __forceinline__ void tile_of(const ProductArgs& p, uint32_t id, uint3
     tn = id % band / high;
 }
 
+// All but the N newest of this wave's loads have landed and its LDS reads are
+// done; then the same holds for every wave.
+template <int N>
+__device__ __forceinline__ void sync_loads() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
 // BM x BN of C by WM x WN waves, one of the splits of the sum (grid y).  LDS
-// holds two stages of 128 along the sum, filled by loads that go from memory to
-// LDS; one barrier a stage.  Row r's 16-byte chunk c sits at c ^ (r / 2 & 7),
+// holds STAGES blocks of 128 along the sum, filled by loads that go from memory
+// to LDS STAGES - 1 blocks ahead; one barrier a block.  Row r's 16-byte chunk c sits at c ^ (r / 2 & 7),
 // which spreads 16 rows' reads of one chunk over all 64 banks; loads into LDS
 // write lanes in order, so the exchange is made on their source addresses.
 // Rows past the matrix repeat its last row; what they give is not stored.
-template <int FA, int FB, bool WIDE, int BM, int BN, int WM, int WN>
+template <int FA, int FB, bool WIDE, int BM, int BN, int WM, int WN, int STAGES>
 __global__ __launch_bounds__(64 * WM * WN) void product_kernel(ProductArgs p) {
     constexpr int NW = WM * WN, SM = BM / WM / 16, SN = BN / WN / 16;
     constexpr int LA = BM / 8 / NW, LB = BN / 8 / NW;
     constexpr int kStage = (BM + BN) * kBlkK, kScales = (BM + BN) * 4;
-    static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0 && BM % 64 == 0 && (BM + BN) / 64 <= NW, "loads per wave");
-    static_assert(NW * finish_bytes<SM, SN>() <= 2 * kStage, "the way out fits the stages");
+    static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0 && BM % 64 == 0 && BN % 64 == 0 && (BM + BN) / 64 <= NW, "loads per wave");
+    static_assert(NW * finish_bytes<SM, SN>() <= STAGES * kStage, "the way out fits the stages");
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-    const uint8_t* scales = lds + 2 * kStage;
+    const uint8_t* scales = lds + STAGES * kStage;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     uint32_t tm, tn;
     tile_of(p, blockIdx.x, tm, tn);
@@ -271,25 +328,29 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(ProductArgs p) {
     const uint32_t os = srow * p.s_pitch;
 
     auto fetch = [&](uint32_t kb) {
-        const uint32_t at = lds0 + (kb & 1) * kStage;
+        const uint32_t at = lds0 + (kb - kb0) % STAGES * kStage;
 #pragma unroll
         for (int i = 0; i < LA; i++) load_lds16(ga + kb * kBlkK, oa[i], at + (wave + i * NW) * 1024);
 #pragma unroll
         for (int i = 0; i < LB; i++) load_lds16(gb + kb * kBlkK, ob[i], at + BM * kBlkK + (wave + i * NW) * 1024);
         if ((kb & 3) == 0 && wave < (BM + BN) / 64)  // four blocks' scale bytes
-            load_lds4(gs + kb, os, lds0 + 2 * kStage + (kb >> 2 & 1) * kScales + wave * 256);
+            load_lds4(gs + kb, os, lds0 + STAGES * kStage + (kb >> 2 & 1) * kScales + wave * 256);
     };
 
     const int wm = wave % WM, wn = wave / WM, row = lane & 15, g = lane >> 4;
     const int c0 = ((2 * g) ^ (row >> 1)) * 16, c1 = ((2 * g + 1) ^ (row >> 1)) * 16;
     v4f acc[SM][SN] = {};
     uint32_t ea[SM], eb[SN];
-    fetch(kb0);
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; s++)
+        if (kb0 + s < kb1) fetch(kb0 + s);
     for (uint32_t kb = kb0; kb < kb1; kb++) {
-        // this wave's loads have landed, then everyone's; and everyone has
-        // read the stage that is filled next
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        if (kb + 1 < kb1) fetch(kb + 1);
+        // block kb has landed, and everyone has read the stage that is filled
+        // next.  A wave that loads scale bytes too waits for one load more.
+        if (kb + STAGES - 2 < kb1) sync_loads<(STAGES - 2) * (LA + LB)>();
+        else sync_loads<0>();
+        if (kb + STAGES - 1 < kb1) fetch(kb + STAGES - 1);
+        const uint8_t* stage = lds + (kb - kb0) % STAGES * kStage;
         if ((kb & 3) == 0) {
             const uint32_t* sc = (const uint32_t*)(scales + (kb >> 2 & 1) * kScales);
 #pragma unroll
@@ -297,8 +358,8 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(ProductArgs p) {
 #pragma unroll
             for (int i = 0; i < SN; i++) eb[i] = sc[BM + (wn * SN + i) * 16 + row];
         }
-        const uint8_t* sa = lds + (kb & 1) * kStage + (wm * SM * 16 + row) * kBlkK;
-        const uint8_t* sb = lds + (kb & 1) * kStage + (BM + wn * SN * 16 + row) * kBlkK;
+        const uint8_t* sa = stage + (wm * SM * 16 + row) * kBlkK;
+        const uint8_t* sb = stage + (BM + wn * SN * 16 + row) * kBlkK;
         v8i fa[SM], fb[SN];
 #pragma unroll
         for (int i = 0; i < SN; i++)
@@ -316,7 +377,7 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(ProductArgs p) {
     }
     __syncthreads();
     finish<SM, SN>(target(p, blockIdx.y), acc, (float*)(lds + wave * finish_bytes<SM, SN>()), m0 + wm * SM * 16,
-                   n0 + wn * SN * 16, lane);
+                   n0 + wn * SN * 16, 0, 0, lane);
 }
 
 // 32 codes from a 16-byte aligned address
@@ -367,7 +428,7 @@ __global__ __launch_bounds__(64 * NW) void product_few_kernel(ProductArgs p) {
 #pragma unroll
             for (int q = 0; q < 8; q++) v[q] += s[q];
         }
-        finish8(p, r, n0 + c, v);
+        finish8(p, r, n0 + c, 0, v);
     }
 }
 
@@ -380,8 +441,19 @@ __global__ __launch_bounds__(256) void product_join_kernel(ProductArgs p, uint32
         const float* s = p.partial + (uint64_t)i * p.n + j;
         const int count = (int)min(p.n - j, 8u);
         float v[8] = {};
-        for (uint32_t z = 0; z < splits; z++) add_row(s + z * plane, count, p.n % 4 == 0, v);
-        finish8(p, i, j, v);
+        for (uint32_t z = 0; z < splits; z++) {
+            if (p.n % 8 == 0) {
+                float w[8];
+                load8(s + z * plane, w);
+#pragma unroll
+                for (int q = 0; q < 8; q++) v[q] += w[q];
+            } else {
+#pragma unroll
+                for (int q = 0; q < 8; q++)
+                    if (q < count) v[q] += s[z * plane + q];
+            }
+        }
+        finish8(p, i, j, 0, v);
     }
 }
 

@@ -309,25 +309,24 @@ def workspace(torch, m, n, k):
 
 def check_product(torch, c, a, b, addend=None, mask=None, p=0.0):
     """c against a b^T (values in 64 bits), within the stated tolerance."""
-    want, s = a @ b.T, np.abs(a) @ np.abs(b).T
-    if mask is not None:
-        want, s = want * mask * F.scale(p), s * mask * F.scale(p)
-    add = 0 if addend is None else host(addend)
-    total = want + add
+    a, b = (torch.from_numpy(np.ascontiguousarray(v)).cuda() for v in (a, b))
+    keep = 1.0 if mask is None else torch.from_numpy(np.ascontiguousarray(mask)).cuda() * F.scale(p)
+    want, s = a @ b.t() * keep, a.abs() @ b.abs().t() * keep
+    total = want if addend is None else want + addend.cuda().double()
     u, low = half_step(torch, c.dtype)
     blocks = -(-a.shape[1] // 128)
     if c.dtype == torch.float32:
         sums = (128 + 2 * blocks) * 2.0**-23 * s
     else:
-        ga, gb = (np.abs(np.pad(v, ((0, 0), (0, -v.shape[1] % 8)))).reshape(len(v), -1, 8).max(2) for v in (a, b))
-        sums = 2.0**-10 * (ga @ gb.T) * (1 if mask is None else mask * F.scale(p)) + (17 * blocks + 64) * 2.0**-23 * s
-    bound = sums + 2.0**-23 * (np.abs(want) + np.abs(total)) + u * np.abs(total) * (1 + 2.0**-6) + low
+        ga, gb = (torch.nn.functional.pad(v.abs(), (0, -v.shape[1] % 8)).unflatten(1, (-1, 8)).amax(2) for v in (a, b))
+        sums = 2.0**-10 * (ga @ gb.t()) * keep + (17 * blocks + 64) * 2.0**-23 * s
+    bound = sums + 2.0**-23 * (want.abs() + total.abs()) + u * total.abs() * (1 + 2.0**-6) + low
     # from half a step above the type's largest value on, rounding gives infinity
-    got, top = host(c), torch.finfo(c.dtype).max * (1 + u / 2)
-    over = np.isinf(got)
-    assert (np.abs(total)[over] + bound[over] >= top).all() and (np.sign(got) == np.sign(total))[over].all()
-    err = np.abs(np.where(over, total, got) - total)
-    assert (err <= bound).all(), ((err - bound).max(), err.max())
+    got, top = c.cuda().double(), torch.finfo(c.dtype).max * (1 + u / 2)
+    over = torch.isinf(got)
+    assert (total.abs()[over] + bound[over] >= top).all() and (got.sign() == total.sign())[over].all()
+    err = torch.where(over, total, got).sub(total).abs()
+    assert (err <= bound).all(), (float((err - bound).max()), float(err.max()))
 
 
 def operands(torch, m, n, k, fa=0, fb=0, seed=0, spread=4):
@@ -354,6 +353,24 @@ def test_product(torch, m, n, k, out):
     c = torch.full((m, n), float("nan"), dtype=dt(torch, out), device="cuda")
     L.demo_block_matmul(L.Product(), m, n, k, a, b, c, workspace=workspace(torch, m, n, k))
     check_product(torch, c, va, vb)
+
+
+@pytest.mark.parametrize("m,n,k,out,fa,fb", [
+    (2000, 8000, 128, "bf16", 0, 0), (2000, 8000, 300, "f16", 1, 0), (1999, 8000, 385, "bf16", 0, 1), (2048, 8192, 520, "bf16", 1, 1),
+    (1801, 7944, 700, "f16", 0, 0), (2000, 8001, 900, "bf16", 0, 0), (1793, 7937, 1100, "f16", 0, 0), (2040, 8184, 2000, "bf16", 0, 0)])
+def test_product_large_tiles(torch, m, n, k, out, fa, fb):
+    """Sizes of the 256 x 256 tiles, whole and moved back at the ends, sums of 1 to 16 blocks."""
+    a, va, b, vb = operands(torch, m, n, k, fa, fb, spread=2)
+    c = torch.full((m, n), float("nan"), dtype=dt(torch, out), device="cuda")
+    cfg = L.Product(fmt_a=fa, fmt_b=fb)
+    L.demo_block_matmul(cfg, m, n, k, a, b, c)
+    check_product(torch, c, va, vb)
+    add = normal(torch, 2, m, n, std=20.0, dtype=c.dtype)
+    drop = dict(p=0.25, seed=5, site=2)
+    L.demo_block_matmul(cfg, m, n, k, a, b, c, addend=add, dropout=L.Dropout(**drop))
+    check_product(torch, c, va, vb, add, F.keep(m * n, **drop).reshape(m, n), 0.25)
+    L.demo_block_matmul(cfg, m, n, k, a, b, add, addend=add, dropout=L.Dropout(**drop))
+    assert torch.equal(add, c)  # in place: no tile adds twice
 
 
 @pytest.mark.parametrize("fa,fb", [(0, 1), (1, 0), (1, 1)])
@@ -443,7 +460,7 @@ def test_product_range_of_scales(torch):
 
 
 def test_product_is_the_same_every_time(torch):
-    for m, n, k in ((1, 512, 4096), (512, 512, 8192), (300, 200, 1000), (2048, 2048, 1024)):
+    for m, n, k in ((1, 512, 4096), (512, 512, 8192), (300, 200, 1000), (2048, 2048, 1024), (2500, 1100, 256)):
         a, _, b, _ = operands(torch, m, n, k)
         ws = workspace(torch, m, n, k)
         c = [torch.empty(m, n, device="cuda") for _ in range(3)]
