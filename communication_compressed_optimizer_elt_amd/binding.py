@@ -9,6 +9,7 @@ raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -261,12 +262,23 @@ def _sends(c) -> bool:
     return c.scheme != SCHEME_DILOCO or (c.period >= 1 and c.step % c.period == c.period - 1)
 
 
+_current = None  # () -> the current stream's handle
+
+
 def _stream(stream) -> int | None:
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
-    import torch
+    global _current
+    if _current is None:
+        import torch
 
-    return torch.cuda.current_stream().cuda_stream
+        # the handle itself where torch gives it: making a Stream object takes 2.7 us
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is None:
+            _current = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+        else:
+            _current = lambda: raw(torch.cuda.current_device())  # noqa: E731
+    return _current()
 
 
 def _cfg(cfg) -> demo_cfg:
@@ -351,29 +363,37 @@ def demo_decode_apply_adamw(cfg, adamw, n_elems: int, params, moment2, payloads,
            "demo_decode_apply_adamw")
 
 
-_DTYPES = {"torch.float32": DTYPE_F32, "torch.float16": DTYPE_F16, "torch.bfloat16": DTYPE_BF16}
+_dtypes: dict = {}  # torch dtype -> DTYPE_*
 
 
 def _dtype(t, what: str) -> int:
-    d = _DTYPES.get(str(t.dtype))
+    d = _dtypes.get(t.dtype)
     if d is None:
-        raise TypeError(f"{what}: expected float32, float16 or bfloat16, got {t.dtype}")
+        import torch
+
+        _dtypes.update({torch.float32: DTYPE_F32, torch.float16: DTYPE_F16, torch.bfloat16: DTYPE_BF16})
+        d = _dtypes.get(t.dtype)
+        if d is None:
+            raise TypeError(f"{what}: expected float32, float16 or bfloat16, got {t.dtype}")
     return d
 
 
-def _here(t, what: str) -> None:
-    """t is on the current device, whose stream the call is queued on."""
-    import torch
-
+def _here(t, what: str) -> int:
+    """The current device, whose stream the call is queued on: t is on it."""
     if not t.is_cuda:
         raise ValueError(f"{what}: expected a device tensor")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{what}: on device {t.device.index}, not the current one")
+    import torch
+
+    dev = torch.cuda.current_device()
+    if t.get_device() != dev:
+        raise ValueError(f"{what}: on device {t.get_device()}, not the current one")
+    return dev
 
 
-def _flat(t, what: str, like) -> int:
-    """Address of a contiguous tensor with like's type and size."""
-    _here(t, what)
+def _flat(t, what: str, like, dev: int) -> int:
+    """Address of a contiguous tensor on device dev with like's type and size."""
+    if t.get_device() != dev:
+        _here(t, what)
     if not t.is_contiguous():
         raise ValueError(f"{what}: expected a contiguous tensor")
     if t.dtype != like.dtype:
@@ -383,27 +403,35 @@ def _flat(t, what: str, like) -> int:
     return t.data_ptr()
 
 
-def _matrix(t, what: str, shape=None, dtype=None) -> tuple[int, int]:
-    """(address, row pitch) of a matrix with neighbouring columns."""
-    _here(t, what)
-    if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
-        raise ValueError(f"{what}: expected a matrix{'' if shape is None else ' of %d x %d' % tuple(shape)}, "
+def _matrix(t, what: str, dev: int, shape=None, dtype=None) -> tuple[int, int]:
+    """(address, row pitch) of a matrix on device dev with neighbouring columns."""
+    if t.get_device() != dev:
+        _here(t, what)
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
+        raise ValueError(f"{what}: expected a matrix{'' if shape is None else ' of %d x %d' % shape}, "
                          f"got {tuple(t.shape)}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{what}: expected {dtype}, got {t.dtype}")
     rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
-        raise ValueError(f"{what}: expected neighbouring columns, got stride {t.stride(1)}")
-    if rows > 1 and t.stride(0) < cols:
-        raise ValueError(f"{what}: rows overlap (row stride {t.stride(0)}, {cols} columns)")
-    return t.data_ptr(), t.stride(0) if rows > 1 else max(cols, 1)
+    pitch, step = t.stride()
+    if cols > 1 and step != 1:
+        raise ValueError(f"{what}: expected neighbouring columns, got stride {step}")
+    if rows > 1 and pitch < cols:
+        raise ValueError(f"{what}: rows overlap (row stride {pitch}, {cols} columns)")
+    return t.data_ptr(), pitch if rows > 1 else max(cols, 1)
 
 
-def _operand_buf(t, what: str, rows: int, cols: int) -> int | None:
+@functools.lru_cache(maxsize=1024)
+def _operand_bytes(rows: int, cols: int) -> int:
+    return demo_block_layout(rows, cols)["total_bytes"]
+
+
+def _operand_buf(t, what: str, rows: int, cols: int, dev: int) -> int | None:
     if t is None:
         return None
-    _here(t, what)
-    return _buf(t, what, demo_block_layout(rows, cols)["total_bytes"])
+    if t.get_device() != dev:
+        _here(t, what)
+    return _buf(t, what, _operand_bytes(rows, cols))
 
 
 def _ref(c):
@@ -413,14 +441,17 @@ def _ref(c):
 def demo_dropout(cfg, x, y, residual=None, stream=None) -> None:
     """y = residual + dropout(x); x, y and residual are contiguous tensors of
     one type and size."""
-    _check(lib().demo_dropout(_ref(cfg), _dtype(x, "x"), x.numel(), _flat(x, "x", x),
-                              None if residual is None else _flat(residual, "residual", x), _flat(y, "y", x),
-                              _stream(stream)), "demo_dropout")
+    dtype, dev = _dtype(x, "x"), _here(x, "x")
+    _check(lib().demo_dropout(_ref(cfg), dtype, x.numel(), _flat(x, "x", x, dev),
+                              None if residual is None else _flat(residual, "residual", x, dev),
+                              _flat(y, "y", x, dev), _stream(stream)), "demo_dropout")
 
 
 def demo_dropout_backward(cfg, dy, dx, stream=None) -> None:
-    _check(lib().demo_dropout_backward(_ref(cfg), _dtype(dy, "dy"), dy.numel(), _flat(dy, "dy", dy),
-                                       _flat(dx, "dx", dy), _stream(stream)), "demo_dropout_backward")
+    """dx = the gradient of demo_dropout for x under the same cfg."""
+    dtype, dev = _dtype(dy, "dy"), _here(dy, "dy")
+    _check(lib().demo_dropout_backward(_ref(cfg), dtype, dy.numel(), _flat(dy, "dy", dy, dev),
+                                       _flat(dx, "dx", dy, dev), _stream(stream)), "demo_dropout_backward")
 
 
 def demo_block_layout(rows: int, cols: int) -> dict:
@@ -433,18 +464,20 @@ def demo_block_quantize(cfg, src, operand=None, operand_t=None, dropout=None, st
     """src: a matrix with neighbouring columns (rows may have a pitch);
     operand and operand_t: device buffers of demo_block_layout(rows, cols) and
     demo_block_layout(cols, rows) bytes."""
-    addr, ld = _matrix(src, "src")
+    dev = _here(src, "src")
+    addr, ld = _matrix(src, "src", dev)
     rows, cols = src.shape
     c = cfg.c(_dtype(src, "src")) if isinstance(cfg, Block) else cfg
     _check(lib().demo_block_quantize(ctypes.byref(c), rows, cols, addr, ld, _ref(dropout),
-                                     _operand_buf(operand, "operand", rows, cols),
-                                     _operand_buf(operand_t, "operand_t", cols, rows), _stream(stream)),
+                                     _operand_buf(operand, "operand", rows, cols, dev),
+                                     _operand_buf(operand_t, "operand_t", cols, rows, dev), _stream(stream)),
            "demo_block_quantize")
 
 
-def demo_block_workspace(cfg, m: int, n: int, k: int) -> int:
+def demo_block_workspace(cfg, m: int, n: int, k: int, dtype: int = DTYPE_F32) -> int:
+    """Bytes of workspace of a product whose result has the type dtype."""
     out = ctypes.c_uint64()
-    c = cfg.c() if isinstance(cfg, Product) else cfg
+    c = cfg.c(dtype) if isinstance(cfg, Product) else cfg
     _check(lib().demo_block_workspace(ctypes.byref(c), m, n, k, ctypes.byref(out)), "demo_block_workspace")
     return int(out.value)
 
@@ -453,15 +486,17 @@ def demo_block_matmul(cfg, m: int, n: int, k: int, a, b, c, addend=None, dropout
                       stream=None) -> None:
     """c = addend + dropout(a b^T) for operands a (m x k) and b (n x k); c and
     addend are m x n matrices of one type with neighbouring columns."""
-    addr, ldc = _matrix(c, "c", (m, n))
-    add, lda = (None, 0) if addend is None else _matrix(addend, "addend", (m, n), c.dtype)
+    dev = _here(c, "c")
+    addr, ldc = _matrix(c, "c", dev, (m, n))
+    add, lda = (None, 0) if addend is None else _matrix(addend, "addend", dev, (m, n), c.dtype)
     cc = cfg.c(_dtype(c, "c")) if isinstance(cfg, Product) else cfg
+    work, have = None, 0
     if workspace is not None:
-        _here(workspace, "workspace")
-    _check(lib().demo_block_matmul(ctypes.byref(cc), m, n, k, _operand_buf(a, "a", m, k),
-                                   _operand_buf(b, "b", n, k), addr, ldc, add, lda, _ref(dropout),
-                                   _buf(workspace, "workspace", 0),
-                                   0 if workspace is None else workspace.numel() * workspace.element_size(),
+        if workspace.get_device() != dev:
+            _here(workspace, "workspace")
+        work, have = _buf(workspace, "workspace", 0), workspace.numel() * workspace.element_size()
+    _check(lib().demo_block_matmul(ctypes.byref(cc), m, n, k, _operand_buf(a, "a", m, k, dev),
+                                   _operand_buf(b, "b", n, k, dev), addr, ldc, add, lda, _ref(dropout), work, have,
                                    _stream(stream)), "demo_block_matmul")
 
 

@@ -26,26 +26,39 @@ struct Drop {
     uint32_t on;
 };
 
-// bit j: element j of the eight of Philox block `blk` is kept
-__device__ __forceinline__ uint32_t keep_block(const Drop& d, uint64_t blk) {
-    uint32_t w[4];
+// the eight draws of Philox block `blk`, two in a word
+__device__ __forceinline__ void draw_block(const Drop& d, uint64_t blk, uint32_t (&w)[4]) {
     philox4x32_10((uint32_t)blk, (uint32_t)(blk >> 32), d.step, d.c3, d.k0, d.k1, w);
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < 4; j++) {
-        m |= (uint32_t)((w[j] & 0xFFFFu) >= d.threshold) << (2 * j);
-        m |= (uint32_t)((w[j] >> 16) >= d.threshold) << (2 * j + 1);
-    }
-    return m;
 }
 
-// bit j: element e + j is kept, j < 8, e counted from the tensor's element 0
-__device__ __forceinline__ uint32_t keep8(const Drop& d, uint64_t e) {
+// v[j] = element j of Philox block `blk` is kept ? v[j] * scale : 0
+__device__ __forceinline__ void drop_block(const Drop& d, uint64_t blk, float (&v)[8]) {
+    uint32_t w[4];
+    draw_block(d, blk, w);
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        v[2 * j] = (w[j] & 0xFFFFu) >= d.threshold ? v[2 * j] * d.scale : 0.f;
+        v[2 * j + 1] = (w[j] >> 16) >= d.threshold ? v[2 * j + 1] * d.scale : 0.f;
+    }
+}
+
+// the same for elements e + j, e counted from the tensor's element 0: they
+// may reach into the next block
+__device__ __forceinline__ void drop8(const Drop& d, uint64_t e, float (&v)[8]) {
     const uint64_t blk = d.first + (e >> 3);
-    const uint32_t sh = (uint32_t)e & 7u;
-    uint32_t m = keep_block(d, blk);
-    if (sh) m = (m | keep_block(d, blk + 1) << 8) >> sh;
-    return m;
+    const uint32_t from = (uint32_t)e & 7u;
+    uint32_t w[4], keep = 0;
+    draw_block(d, blk, w);
+#pragma unroll
+    for (int j = 0; j < 8; j++) keep |= (uint32_t)((w[j >> 1] >> 16 * (j & 1) & 0xFFFFu) >= d.threshold) << j;
+    if (from) {
+        draw_block(d, blk + 1, w);
+#pragma unroll
+        for (int j = 0; j < 8; j++) keep |= (uint32_t)((w[j >> 1] >> 16 * (j & 1) & 0xFFFFu) >= d.threshold) << (8 + j);
+    }
+    keep >>= from;
+#pragma unroll
+    for (int j = 0; j < 8; j++) v[j] = keep >> j & 1 ? v[j] * d.scale : 0.f;
 }
 
 struct DropoutArgs {
@@ -71,20 +84,21 @@ __global__ __launch_bounds__(256) void dropout_kernel(DropoutArgs p) {
             float v[8], r[8];
             load8(x + e, v);
             if (RES) load8(res + e, r);
-            const uint32_t keep = keep_block(p.drop, p.drop.first + b);
+            drop_block(p.drop, p.drop.first + b, v);
+            if (RES) {
 #pragma unroll
-            for (int j = 0; j < 8; j++) {
-                v[j] = keep >> j & 1 ? v[j] * p.drop.scale : 0.f;
-                if (RES) v[j] += r[j];
+                for (int j = 0; j < 8; j++) v[j] += r[j];
             }
             store8(y + e, v);
         } else {
-            const uint32_t keep = keep_block(p.drop, p.drop.first + b);
-            for (int j = 0; e + j < p.n; j++) {
-                float v = keep >> j & 1 ? to_float(x[e + j]) * p.drop.scale : 0.f;
-                if (RES) v += to_float(res[e + j]);
-                y[e + j] = from_float<T>(v);
-            }
+            float v[8];
+            const int left = (int)(p.n - e);
+#pragma unroll
+            for (int j = 0; j < 8; j++) v[j] = j < left ? to_float(x[e + j]) : 0.f;
+            drop_block(p.drop, p.drop.first + b, v);
+#pragma unroll
+            for (int j = 0; j < 8; j++)
+                if (j < left) y[e + j] = from_float<T>(RES ? v[j] + to_float(res[e + j]) : v[j]);
         }
     }
 }

@@ -88,8 +88,11 @@ int dropout_impl(const demo_dropout_cfg* cfg, uint32_t dtype, uint64_t n, const 
 
 template <typename T, int FMT>
 hipError_t launch_quantize(const demo::QuantArgs& a, bool tile, dim3 grid, hipStream_t s) {
-    return launch(tile ? demo::quantize_kernel<T, FMT, true> : demo::quantize_kernel<T, FMT, false>, grid, dim3(256), 0,
-                  s, a);
+    if (a.drop.on)
+        return launch(tile ? demo::quantize_kernel<T, FMT, true, true> : demo::quantize_kernel<T, FMT, false, true>, grid,
+                      dim3(256), 0, s, a);
+    return launch(tile ? demo::quantize_kernel<T, FMT, true, false> : demo::quantize_kernel<T, FMT, false, false>, grid,
+                  dim3(256), 0, s, a);
 }
 
 template <typename T>
@@ -108,10 +111,10 @@ int check_product(const demo_product_cfg* cfg, uint64_t m, uint64_t n, uint64_t 
     return DEMO_OK;
 }
 
-constexpr uint64_t kFewRows = 64;
+constexpr uint64_t kFewRows = 16;
 
 // How a product is cut: tiles of `tile` x `tile` and `splits` of the sum, or
-// (tile 0) the kernel for few rows.
+// (tile 0) the kernels for few rows.
 struct Plan {
     uint32_t tile;
     uint32_t splits;
@@ -159,11 +162,9 @@ hipError_t launch_tiles(const demo::ProductArgs& a, dim3 grid, hipStream_t s) {
 template <int FA, int FB, bool WIDE>
 hipError_t launch_product(demo::ProductArgs a, const Plan& plan, void* workspace, hipStream_t s) {
     if (plan.tile == 0) {
-        const dim3 grid((a.n + 15) / 16);
-        constexpr int NW = 16;
-        if (a.m <= 16) return launch(demo::product_few_kernel<FA, FB, WIDE, 1, NW>, grid, dim3(64 * NW), 0, s, a);
-        if (a.m <= 32) return launch(demo::product_few_kernel<FA, FB, WIDE, 2, NW>, grid, dim3(64 * NW), 0, s, a);
-        return launch(demo::product_few_kernel<FA, FB, WIDE, 4, 8>, grid, dim3(64 * 8), 0, s, a);
+        if (a.m == 1) return launch(demo::product_rows_kernel<FA, FB, 1>, dim3((a.n + 3) / 4), dim3(256), 0, s, a);
+        if (a.m == 2) return launch(demo::product_rows_kernel<FA, FB, 2>, dim3((a.n + 3) / 4), dim3(256), 0, s, a);
+        return launch(demo::product_few_kernel<FA, FB, WIDE, 8>, dim3((a.n + 15) / 16), dim3(512), 0, s, a);
     }
     a.kb_split = plan.kb_split;
     a.partial = plan.splits > 1 ? static_cast<float*>(workspace) : nullptr;

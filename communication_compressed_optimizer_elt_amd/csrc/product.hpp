@@ -60,10 +60,11 @@ __device__ __forceinline__ void load_lds4(const uint8_t* base, uint32_t offset, 
 // C[i, j+from..j+7] from eight sums: drop, add, round once, store, element by
 // element or (wide, from 0, eight left) in aligned accesses
 template <typename T>
-__device__ __forceinline__ void put_row(const ProductArgs& p, uint32_t i, uint32_t j, int from, int count, float (&v)[8]) {
+__device__ __forceinline__ void put_row(const ProductArgs& p, uint32_t i, uint32_t j, int from, int count, float (&v)[8],
+                                        bool wide) {
     T* c = (T*)p.c + (uint64_t)i * p.ldc + j;
     const T* add = (const T*)p.addend + (p.addend ? (uint64_t)i * p.ld_addend + j : 0);
-    if (p.wide) {
+    if (wide) {
         if (p.addend) {
             float w[8];
             load8(add, w);
@@ -82,13 +83,11 @@ __device__ __forceinline__ void finish8(const ProductArgs& p, uint32_t i, uint32
     if (i >= p.m || j >= p.n) return;
     const int count = (int)min(p.n - j, 8u);
     if (p.drop.on) {
-        const uint32_t keep = keep8(p.drop, (uint64_t)i * p.n + j);
-#pragma unroll
-        for (int q = 0; q < 8; q++) v[q] = keep >> q & 1 ? v[q] * p.drop.scale : 0.f;
+        drop8(p.drop, (uint64_t)i * p.n + j, v);
     }
-    if (p.dtype == kF32) put_row<float>(p, i, j, from, count, v);
-    else if (p.dtype == kF16) put_row<f16_t>(p, i, j, from, count, v);
-    else put_row<bf16_t>(p, i, j, from, count, v);
+    if (p.dtype == kF32) put_row<float>(p, i, j, from, count, v, p.wide);
+    else if (p.dtype == kF16) put_row<f16_t>(p, i, j, from, count, v, p.wide);
+    else put_row<bf16_t>(p, i, j, from, count, v, p.wide);
 }
 
 // eight raw neighbours of a row
@@ -163,11 +162,8 @@ __device__ __forceinline__ void finish(const ProductArgs& p, const v4f (&acc)[SM
             }
             if (p.drop.on) {
 #pragma unroll
-                for (int r = 0; r < P; r++) {
-                    const uint32_t keep = keep_block(p.drop, p.drop.first + ((i[r] * p.n + j) >> 3));
-#pragma unroll
-                    for (int q = 0; q < 8; q++) v[r][q] = keep >> q & 1 ? v[r][q] * p.drop.scale : 0.f;
-                }
+                for (int r = 0; r < P; r++)
+                    drop_block(p.drop, p.drop.first + ((i[r] * p.n + j) >> 3), v[r]);
             }
             if (p.dtype == kF32) finish_rows<float, P>(p, i, j, on, v);
             else if (p.dtype == kF16) finish_rows<f16_t, P>(p, i, j, on, v);
@@ -385,50 +381,97 @@ __device__ __forceinline__ v8i load_codes(const uint8_t* p) {
     return __builtin_shufflevector(*(const v4i*)p, *(const v4i*)(p + 16), 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-// Few rows: 16 columns of C for up to 16 SM rows by NW waves that share the
-// sum among them, each taking every NW-th block of 128 straight from memory
-// (nothing is used twice), and add up in LDS in the order of the waves.
-template <int FA, int FB, bool WIDE, int SM, int NW>
+// Few rows: 16 columns of C for up to 16 rows by NW waves that share the sum
+// among them, each taking every NW-th block of 128 straight from memory
+// (nothing is used twice), and add up in LDS in the order of the waves.  Bound
+// by the latency of the one or two loads that a wave has in turn: 16 x 2048 x
+// 8192 takes 12.8 us (13.1 with 16 waves), 16 x 8192 x 2048 6.9 us.
+template <int FA, int FB, bool WIDE, int NW>
 __global__ __launch_bounds__(64 * NW) void product_few_kernel(ProductArgs p) {
-    __shared__ __attribute__((aligned(16))) float sums[NW][SM][16 * 20];
+    __shared__ __attribute__((aligned(16))) float sums[NW][16 * 20];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, row = lane & 15, g = lane >> 4;
     const uint32_t n0 = blockIdx.x * 16;
-    const uint32_t rb = min(n0 + row, p.n - 1);
-    const uint8_t* qb = p.b + (uint64_t)rb * p.pitch + g * 32;
-    const uint8_t* xb = p.sb + (uint64_t)rb * p.s_pitch;
-    const uint8_t *qa[SM], *xa[SM];
-#pragma unroll
-    for (int i = 0; i < SM; i++) {
-        const uint32_t ra = min((uint32_t)(i * 16 + row), p.m - 1);
-        qa[i] = p.a + (uint64_t)ra * p.pitch + g * 32;
-        xa[i] = p.sa + (uint64_t)ra * p.s_pitch;
-    }
-    v4f acc[SM][1] = {};
+    const uint32_t ra = min((uint32_t)row, p.m - 1), rb = min(n0 + row, p.n - 1);
+    const uint8_t *qa = p.a + (uint64_t)ra * p.pitch + g * 32, *xa = p.sa + (uint64_t)ra * p.s_pitch;
+    const uint8_t *qb = p.b + (uint64_t)rb * p.pitch + g * 32, *xb = p.sb + (uint64_t)rb * p.s_pitch;
+    v4f acc[1][1] = {};
 #pragma unroll 4
     for (uint32_t kb = wave; kb < p.kb; kb += NW) {
-        v8i fa[SM], fb[1];
-        uint32_t ea[SM], eb[1] = {xb[kb]};
-        fb[0] = load_codes(qb + kb * kBlkK);
-#pragma unroll
-        for (int i = 0; i < SM; i++) {
-            fa[i] = load_codes(qa[i] + kb * kBlkK);
-            ea[i] = xa[i][kb];
-        }
+        const uint32_t ea[1] = {xa[kb]}, eb[1] = {xb[kb]};
+        const v8i fa[1] = {load_codes(qa + kb * kBlkK)}, fb[1] = {load_codes(qb + kb * kBlkK)};
         multiply<FA, FB, WIDE>(acc, fa, fb, ea, eb);
     }
-#pragma unroll
-    for (int i = 0; i < SM; i++) *(v4f*)&sums[wave][i][row * 20 + 4 * g] = acc[i][0];
+    *(v4f*)&sums[wave][row * 20 + 4 * g] = acc[0][0];
     __syncthreads();
-    // two lanes a row, eight columns each
-    for (uint32_t t = threadIdx.x; t < SM * 32; t += 64 * NW) {
-        const uint32_t r = t >> 1, c = (t & 1) * 8;
+    if (threadIdx.x < 32) {  // two lanes a row, eight columns each
+        const uint32_t r = threadIdx.x >> 1, c = (threadIdx.x & 1) * 8;
         float v[8] = {};
         for (int w = 0; w < NW; w++) {
-            const float* s = &sums[w][r >> 4][(r & 15) * 20 + c];
+            const float* s = &sums[w][r * 20 + c];
 #pragma unroll
             for (int q = 0; q < 8; q++) v[q] += s[q];
         }
         finish8(p, r, n0 + c, 0, v);
+    }
+}
+
+// two floats of two codes
+template <int FMT, bool HI>
+__device__ __forceinline__ void floats2(uint32_t w, float& x, float& y) {
+    typedef float v2f __attribute__((ext_vector_type(2)));
+    const v2f r = FMT == kE4M3 ? __builtin_amdgcn_cvt_pk_f32_fp8((int)w, HI) : __builtin_amdgcn_cvt_pk_f32_bf8((int)w, HI);
+    x = r[0], y = r[1];
+}
+
+// One or two rows, as a token at a time makes them: a wave for each column of
+// C, its lanes along the sum, 16 codes each, in fp32; the eight lanes of a
+// block of 128 scale what they have of it.  No matrix instruction, whose other
+// 15 rows would be empty: one row x 2048 x 8192 takes 5.8 us against 8.5 us of
+// product_few_kernel, 16384 x 8192 24.7 against 29.7 us (5.4 TB/s of codes);
+// two rows 6.1 against 9.0 us; at four rows the gain is gone (8.2, 9.7 us, and
+// 7.3 against 5.4 us with 8192 columns of 2048).
+template <int FA, int FB, int M>
+__global__ __launch_bounds__(256) void product_rows_kernel(ProductArgs p) {
+    const int lane = threadIdx.x & 63;
+    const uint32_t j = blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (j >= p.n) return;
+    const uint8_t *qb = p.b + (uint64_t)j * p.pitch, *xb = p.sb + (uint64_t)j * p.s_pitch;
+    float sum[M] = {};
+#pragma unroll(M == 1 ? 8 : 4)
+    for (uint32_t k = lane * 16; k < p.pitch; k += 1024) {
+        const v4i b = *(const v4i*)(qb + k);
+        const int eb = xb[k >> 7];
+        v4i a[M];
+        int ea[M];
+#pragma unroll
+        for (int i = 0; i < M; i++) {
+            a[i] = *(const v4i*)(p.a + (uint64_t)i * p.pitch + k);
+            ea[i] = p.sa[(uint64_t)i * p.s_pitch + (k >> 7)];
+        }
+#pragma unroll
+        for (int i = 0; i < M; i++) {
+            float s = 0.f;
+#pragma unroll
+            for (int w = 0; w < 4; w++) {
+                float x[4], y[4];
+                floats2<FA, false>(a[i][w], x[0], x[1]), floats2<FA, true>(a[i][w], x[2], x[3]);
+                floats2<FB, false>(b[w], y[0], y[1]), floats2<FB, true>(b[w], y[2], y[3]);
+#pragma unroll
+                for (int q = 0; q < 4; q++) s = fmaf(x[q], y[q], s);
+            }
+            sum[i] += ldexpf(s, ea[i] + eb - 254);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < M; i++)
+#pragma unroll
+        for (int d = 32; d; d >>= 1) sum[i] += __shfl_xor(sum[i], d);
+    if (lane < M) {
+        float v[8] = {M > 1 && lane ? sum[M - 1] : sum[0]};
+        if (p.drop.on) drop8(p.drop, (uint64_t)lane * p.n + j, v);
+        if (p.dtype == kF32) put_row<float>(p, lane, j, 0, 1, v, false);
+        else if (p.dtype == kF16) put_row<f16_t>(p, lane, j, 0, 1, v, false);
+        else put_row<bf16_t>(p, lane, j, 0, 1, v, false);
     }
 }
 

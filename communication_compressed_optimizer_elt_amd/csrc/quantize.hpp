@@ -14,6 +14,8 @@
 // through 16-lane exchanges (rows) and a small LDS table (columns).
 #pragma once
 
+#include <type_traits>
+
 #include "dropout.hpp"
 
 namespace demo {
@@ -35,122 +37,326 @@ struct QuantArgs {
     Drop drop;
 };
 
-// magnitude bits of a finite value, 0 for infinity and NaN
-__device__ __forceinline__ uint32_t finite_bits(float x) {
-    const uint32_t u = __float_as_uint(x) & 0x7FFFFFFFu;
-    return u < 0x7F800000u ? u : 0u;
-}
-
-// scale byte of a block whose largest finite magnitude has the bits u
+// scale byte of a block whose largest finite magnitude has the fp32 bits u
 template <int FMT>
 __device__ __forceinline__ uint32_t scale_byte(uint32_t u) {
     const int b = (int)(u >> 23) - (FMT == kE4M3 ? 8 : 15) + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0);
     return (uint32_t)max(b, 0);
 }
 
-// 2^-e of a scale byte e + 127 <= 247
-__device__ __forceinline__ float inverse_scale(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
+// the scale of a byte
+__device__ __forceinline__ float scale_of(uint32_t byte) { return __uint_as_float(byte ? byte << 23 : 0x00400000u); }
 
-__device__ __forceinline__ uint32_t max16(uint32_t u) {  // over 16 neighbouring lanes
-#pragma unroll
-    for (int s = 1; s < 16; s <<= 1) u = max(u, (uint32_t)__shfl_xor((int)u, s));
-    return u;
+// maxima over 16 neighbouring lanes, and over the wave's four lanes of equal l % 16
+template <int CTRL>
+__device__ __forceinline__ uint32_t max_dpp(uint32_t u) {
+    return max(u, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)u, CTRL, 0xF, 0xF, true));
+}
+__device__ __forceinline__ uint32_t max16(uint32_t u) {
+    u = max_dpp<0xB1>(u);   // lanes 1 0 3 2
+    u = max_dpp<0x4E>(u);   // lanes 2 3 0 1
+    u = max_dpp<0x141>(u);  // halves of a row mirrored
+    return max_dpp<0x140>(u);  // rows mirrored
+}
+typedef uint32_t uint2_s __attribute__((ext_vector_type(2)));
+typedef uint16_t us2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t pk_max(uint32_t a, uint32_t b) {
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(us2, a), __builtin_bit_cast(us2, b)));
+}
+template <bool PACKED>
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+    return PACKED ? pk_max(a, b) : max(a, b);
+}
+template <bool PACKED>
+__device__ __forceinline__ uint32_t max_rows(uint32_t u) {
+    uint2_s r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    u = larger<PACKED>(r[0], r[1]);
+    r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    return larger<PACKED>(r[0], r[1]);
 }
 
-template <typename T, int FMT, bool TILE>
-__global__ __launch_bounds__(256) void quantize_kernel(QuantArgs p) {
-    __shared__ uint32_t colmax[4][kBlk];
-    __shared__ __attribute__((aligned(16))) uint8_t turned[kBlk * kBlk];
-    const int t = threadIdx.x, g = t >> 4, h = t & 15, wave = t >> 6;
-    const uint32_t tc = blockIdx.x % p.tiles_c, tr = blockIdx.x / p.tiles_c;
-    const uint32_t r0 = tr * kBlk + g * 8, c0 = tc * kBlk + h * 8;
-
-    float v[8][8];
-#pragma unroll
-    for (int i = 0; i < 8; i++) {
-        const uint32_t r = r0 + i;
-#pragma unroll
-        for (int j = 0; j < 8; j++) v[i][j] = 0.f;
-        if (r < p.rows && c0 < p.cols) {
-            const T* src = (const T*)p.src + (uint64_t)r * p.ld + c0;
-            if (p.wide) {
-                load8(src, v[i]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; j++)
-                    if (c0 + j < p.cols) v[i][j] = to_float(src[j]);
-            }
-        }
+// Two codes, of values over a scale 2^e, into half HI of a word.  The
+// hardware divides and rounds once, to nearest even; its scale is the
+// exponent of the float.
+typedef short s2 __attribute__((ext_vector_type(2)));
+typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+template <int FMT, bool HI>
+__device__ __forceinline__ s2 codes2(s2 old, float x, float y, float scale) {
+    return FMT == kE4M3 ? __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(old, x, y, scale, HI)
+                        : __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(old, x, y, scale, HI);
+}
+template <int FMT, bool HI, typename T>
+__device__ __forceinline__ s2 codes2(s2 old, uint32_t pair, float scale) {
+    if constexpr (sizeof(T) == 2 && __is_same(T, bf16_t)) {
+        const b2 v = __builtin_bit_cast(b2, pair);
+        return FMT == kE4M3 ? __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(old, v, scale, HI)
+                            : __builtin_amdgcn_cvt_scalef32_pk_bf8_bf16(old, v, scale, HI);
+    } else {
+        const h2 v = __builtin_bit_cast(h2, pair);
+        return FMT == kE4M3 ? __builtin_amdgcn_cvt_scalef32_pk_fp8_f16(old, v, scale, HI)
+                            : __builtin_amdgcn_cvt_scalef32_pk_bf8_f16(old, v, scale, HI);
     }
-    if (p.drop.on) {
+}
+
+// A work-item's 8 x 8 values as floats (fp32 sources, and what a dropout has
+// scaled): magnitudes are compared as fp32 bits.
+struct FloatSquare {
+    static constexpr bool kPacked = false;
+    float v[8][8];
+
+    static __device__ __forceinline__ bool odd(uint32_t u) { return u >= 0x7F800000u; }  // infinity or NaN
+    // magnitude; FINITE: 0 for infinity and NaN
+    template <bool FINITE>
+    __device__ __forceinline__ uint32_t size(int i, int j) const {
+        const uint32_t u = __float_as_uint(v[i][j]) & 0x7FFFFFFFu;
+        return FINITE && odd(u) ? 0u : u;
+    }
+    // maxima of the rows and of the columns, words of 32 bits
+    template <bool FINITE>
+    __device__ __forceinline__ void maxima(uint32_t (&r)[8], uint32_t (&c)[8]) const {
 #pragma unroll
         for (int i = 0; i < 8; i++) {
-            const uint32_t r = r0 + i;
-            if (r < p.rows && c0 < p.cols) {
-                const uint32_t keep = keep8(p.drop, (uint64_t)r * p.cols + c0);
+            r[i] = 0;
 #pragma unroll
-                for (int j = 0; j < 8; j++) v[i][j] = keep >> j & 1 ? v[i][j] * p.drop.scale : 0.f;
+            for (int j = 0; j < 8; j++) {
+                const uint32_t u = size<FINITE>(i, j);
+                r[i] = max(r[i], u);
+                c[j] = i ? max(c[j], u) : u;
             }
         }
     }
-    // infinities become NaN here, so that both formats store NaN for them
-    uint32_t rowmax[8], cmax[8];
+    // the rare path computes from the values again instead of keeping what
+    // the usual one had of them in registers
+    __device__ __forceinline__ void renew() {
 #pragma unroll
-    for (int j = 0; j < 8; j++) cmax[j] = 0;
+        for (int i = 0; i < 8; i++)
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
-        rowmax[i] = 0;
+            for (int j = 0; j < 8; j++) asm volatile("" : "+v"(v[i][j]));
+    }
+    __device__ __forceinline__ void infinities_to_nan() {
 #pragma unroll
-        for (int j = 0; j < 8; j++) {
-            const uint32_t u = finite_bits(v[i][j]);
-            if ((__float_as_uint(v[i][j]) & 0x7F800000u) == 0x7F800000u) v[i][j] = __uint_as_float(0x7FC00000u);
-            rowmax[i] = max(rowmax[i], u);
-            cmax[j] = max(cmax[j], u);
+        for (int i = 0; i < 8; i++)
+#pragma unroll
+            for (int j = 0; j < 8; j++)
+                if (odd(__float_as_uint(v[i][j]) & 0x7FFFFFFFu)) v[i][j] = __uint_as_float(0x7FC00000u);
+    }
+    template <int FMT>
+    __device__ __forceinline__ uint2_v row_codes(int i, float k) const {
+        s2 a = {}, b = {};
+        a = codes2<FMT, false>(a, v[i][0], v[i][1], k), a = codes2<FMT, true>(a, v[i][2], v[i][3], k);
+        b = codes2<FMT, false>(b, v[i][4], v[i][5], k), b = codes2<FMT, true>(b, v[i][6], v[i][7], k);
+        return uint2_v{__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b)};
+    }
+    template <int FMT>
+    __device__ __forceinline__ uint2_v col_codes(int j, float k) const {
+        s2 a = {}, b = {};
+        a = codes2<FMT, false>(a, v[0][j], v[1][j], k), a = codes2<FMT, true>(a, v[2][j], v[3][j], k);
+        b = codes2<FMT, false>(b, v[4][j], v[5][j], k), b = codes2<FMT, true>(b, v[6][j], v[7][j], k);
+        return uint2_v{__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b)};
+    }
+};
+
+// The same as pairs of 16-bit values of a row: magnitudes are compared as
+// their own bits, two at a time.
+template <typename T>
+struct PairSquare {
+    static constexpr bool kPacked = true;
+    static constexpr uint32_t kInf = __is_same(T, bf16_t) ? 0x7F80u : 0x7C00u;
+    uint32_t v[8][4];
+
+    static __device__ __forceinline__ bool odd(uint32_t u) { return (u & 0x7FFFu) >= kInf || (u >> 16 & 0x7FFFu) >= kInf; }
+    template <bool FINITE>
+    __device__ __forceinline__ uint32_t size(int i, int j) const {
+        uint32_t u = v[i][j] & 0x7FFF7FFFu;
+        if (FINITE && (u & 0xFFFFu) >= kInf) u &= 0xFFFF0000u;
+        if (FINITE && (u >> 16) >= kInf) u &= 0xFFFFu;
+        return u;
+    }
+    // maxima of the rows, and of the columns as pairs
+    template <bool FINITE>
+    __device__ __forceinline__ void maxima(uint32_t (&r)[8], uint32_t (&c)[4]) const {
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            uint32_t row = 0;
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const uint32_t u = size<FINITE>(i, j);
+                row = j ? pk_max(row, u) : u;
+                c[j] = i ? pk_max(c[j], u) : u;
+            }
+            r[i] = max(row & 0xFFFFu, row >> 16);
         }
+    }
+    static __device__ __forceinline__ float number(uint32_t u) { return (float)__builtin_bit_cast(T, (uint16_t)u); }
+    __device__ __forceinline__ void renew() {
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+#pragma unroll
+            for (int j = 0; j < 4; j++) asm volatile("" : "+v"(v[i][j]));
+    }
+    __device__ __forceinline__ void infinities_to_nan() {
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                if ((v[i][j] & 0x7FFFu) >= kInf) v[i][j] |= 0x7FFFu;
+                if ((v[i][j] >> 16 & 0x7FFFu) >= kInf) v[i][j] |= 0x7FFF0000u;
+            }
+    }
+    template <int FMT>
+    __device__ __forceinline__ uint2_v row_codes(int i, float k) const {
+        s2 a = {}, b = {};
+        a = codes2<FMT, false, T>(a, v[i][0], k), a = codes2<FMT, true, T>(a, v[i][1], k);
+        b = codes2<FMT, false, T>(b, v[i][2], k), b = codes2<FMT, true, T>(b, v[i][3], k);
+        return uint2_v{__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b)};
+    }
+    // column j of rows i, i + 1 as a pair
+    __device__ __forceinline__ uint32_t down(int i, int j) const {
+        return __builtin_amdgcn_perm(v[i + 1][j >> 1], v[i][j >> 1], j & 1 ? 0x07060302u : 0x05040100u);
+    }
+    template <int FMT>
+    __device__ __forceinline__ uint2_v col_codes(int j, float k) const {
+        s2 a = {}, b = {};
+        a = codes2<FMT, false, T>(a, down(0, j), k), a = codes2<FMT, true, T>(a, down(2, j), k);
+        b = codes2<FMT, false, T>(b, down(4, j), k), b = codes2<FMT, true, T>(b, down(6, j), k);
+        return uint2_v{__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b)};
+    }
+};
+
+template <typename T>
+struct Square : PairSquare<T> {};
+template <>
+struct Square<float> : FloatSquare {};
+
+// Eight neighbours of a row from 0-bits on: pairs or floats
+template <typename T>
+__device__ __forceinline__ void load_row(const T* src, bool wide, uint32_t left, uint32_t (&v)[4]) {
+    if (wide) {
+        const uint4_v w = *(const uint4_v*)src;
+#pragma unroll
+        for (int j = 0; j < 4; j++) v[j] = w[j];
+    } else {
+        const uint16_t* s = (const uint16_t*)src;
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            if ((uint32_t)j < left) v[j >> 1] |= (uint32_t)s[j] << 16 * (j & 1);
+    }
+}
+__device__ __forceinline__ void load_row(const float* src, bool wide, uint32_t left, float (&v)[8]) {
+    if (wide) {
+        load8(src, v);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            if ((uint32_t)j < left) v[j] = src[j];
+    }
+}
+
+// fp32 bits of a maximum as the square keeps it
+template <typename SQ, typename T>
+__device__ __forceinline__ uint32_t float_bits(uint32_t u) {
+    if constexpr (SQ::kPacked) return __float_as_uint(SQ::number(u));
+    else return u;
+}
+
+// DROP: the source through a dropout's gradient, as floats.
+template <typename T, int FMT, bool TILE, bool DROP>
+__global__ __launch_bounds__(256, 4) void quantize_kernel(QuantArgs p) {
+    typedef typename std::conditional<DROP, FloatSquare, Square<T>>::type SQ;
+    constexpr int kCols = SQ::kPacked ? 4 : 8;  // words of a work-item's columns' maxima
+    __shared__ __attribute__((aligned(16))) uint32_t colmax[4][16 * kCols];
+    __shared__ __attribute__((aligned(16))) uint8_t turned[kBlk * kBlk];
+    const int t = threadIdx.x, g = t >> 4, h = t & 15, wave = t >> 6;
+    // neighbouring squares go to one XCD, whose L2 gathers their single scale bytes
+    const uint32_t q8 = gridDim.x / kXcds, r8 = gridDim.x % kXcds, x8 = blockIdx.x % kXcds;
+    const uint32_t id = x8 * q8 + min(x8, r8) + blockIdx.x / kXcds;
+    const uint32_t tc = id % p.tiles_c, tr = id / p.tiles_c;
+    const uint32_t r0 = tr * kBlk + g * 8, c0 = tc * kBlk + h * 8;
+
+    SQ sq;
+    {
+        Square<T> raw;
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+#pragma unroll
+            for (int j = 0; j < (Square<T>::kPacked ? 4 : 8); j++) raw.v[i][j] = 0;
+            if (r0 + i < p.rows && c0 < p.cols)
+                load_row((const T*)p.src + (uint64_t)(r0 + i) * p.ld + c0, p.wide, p.cols - c0, raw.v[i]);
+        }
+        if constexpr (!DROP) {
+            static_cast<Square<T>&>(sq) = raw;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+#pragma unroll
+                for (int j = 0; j < 8; j++) {
+                    if constexpr (Square<T>::kPacked) sq.v[i][j] = Square<T>::number(raw.v[i][j >> 1] >> 16 * (j & 1));
+                    else sq.v[i][j] = raw.v[i][j];
+                }
+                const uint64_t e = (uint64_t)(r0 + i) * p.cols + c0;
+                if (p.cols % 8 == 0) drop_block(p.drop, p.drop.first + (e >> 3), sq.v[i]);
+                else drop8(p.drop, e, sq.v[i]);
+            }
+        }
+    }
+    uint32_t rowmax[8], cmax[kCols], any = 0;
+    sq.template maxima<false>(rowmax, cmax);
+#pragma unroll
+    for (int j = 0; j < kCols; j++) any |= SQ::odd(cmax[j]);
+    if (any) {  // infinities and NaN: no part of a maximum, and NaN in the end
+        sq.renew();
+        sq.template maxima<true>(rowmax, cmax);
+        sq.infinities_to_nan();
     }
 #pragma unroll
     for (int i = 0; i < 8; i++) rowmax[i] = max16(rowmax[i]);
+    auto rows_out = [&] {
+        if (p.q) {
 #pragma unroll
-    for (int j = 0; j < 8; j++) {
-        cmax[j] = max(cmax[j], (uint32_t)__shfl_xor((int)cmax[j], 16));
-        cmax[j] = max(cmax[j], (uint32_t)__shfl_xor((int)cmax[j], 32));
-    }
-    if ((t & 63) < 16) {
-#pragma unroll
-        for (int j = 0; j < 8; j++) colmax[wave][h * 8 + j] = cmax[j];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < 8; j++) {
-        const int c = h * 8 + j;
-        cmax[j] = max(max(colmax[0][c], colmax[1][c]), max(colmax[2][c], colmax[3][c]));
-    }
-    if (TILE) {
-        uint32_t all = 0;
-#pragma unroll
-        for (int j = 0; j < 8; j++) all = max(all, cmax[j]);
-        all = max16(all);
-#pragma unroll
-        for (int j = 0; j < 8; j++) cmax[j] = rowmax[j] = all;
-    }
-    if (p.q) {
-#pragma unroll
-        for (int i = 0; i < 8; i++) {
-            const uint32_t r = r0 + i, b = scale_byte<FMT>(rowmax[i]);
-            const float k = inverse_scale(b);
-            if (r < p.rows) {
-                const uint32_t lo = codes4<FMT>(v[i][0] * k, v[i][1] * k, v[i][2] * k, v[i][3] * k);
-                const uint32_t hi = codes4<FMT>(v[i][4] * k, v[i][5] * k, v[i][6] * k, v[i][7] * k);
-                *(uint2_v*)(p.q + (uint64_t)r * p.pitch + c0) = uint2_v{lo, hi};
-                if (h == 0) {
-                    uint8_t* s = p.s + (uint64_t)r * p.s_pitch;
-                    s[tc] = (uint8_t)b;
-                    if (tc + 1 == p.tiles_c)
-                        for (uint32_t c = tc + 1; c < p.s_pitch; c++) s[c] = 0;
+            for (int i = 0; i < 8; i++) {
+                const uint32_t r = r0 + i, b = scale_byte<FMT>(float_bits<SQ, T>(rowmax[i]));
+                if (r < p.rows) {
+                    *(uint2_v*)(p.q + (uint64_t)r * p.pitch + c0) = sq.template row_codes<FMT>(i, scale_of(b));
+                    if (h == 0) {
+                        uint8_t* s = p.s + (uint64_t)r * p.s_pitch;
+                        s[tc] = (uint8_t)b;
+                        if (tc + 1 == p.tiles_c)
+                            for (uint32_t c = tc + 1; c < p.s_pitch; c++) s[c] = 0;
+                    }
                 }
             }
         }
+    };
+    if (!TILE) rows_out();
+#pragma unroll
+    for (int j = 0; j < kCols; j++) cmax[j] = max_rows<SQ::kPacked>(cmax[j]);
+    if ((t & 63) < 16) {
+#pragma unroll
+        for (int j = 0; j < kCols; j += 4)
+            *(uint4_v*)&colmax[wave][h * kCols + j] = uint4_v{cmax[j], cmax[j + 1], cmax[j + 2], cmax[j + 3]};
     }
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 4; w++)
+#pragma unroll
+        for (int j = 0; j < kCols; j += 4) {
+            const uint4_v o = *(const uint4_v*)&colmax[w][h * kCols + j];
+#pragma unroll
+            for (int q = 0; q < 4; q++) cmax[j + q] = larger<SQ::kPacked>(cmax[j + q], o[q]);
+        }
+    uint32_t colbits[8];
+#pragma unroll
+    for (int j = 0; j < 8; j++) colbits[j] = SQ::kPacked ? cmax[j / 2 % kCols] >> 16 * (j & 1) & 0xFFFFu : cmax[j % kCols];
+    if (TILE) {
+        uint32_t all = 0;
+#pragma unroll
+        for (int j = 0; j < 8; j++) all = max(all, colbits[j]);
+        all = max16(all);
+#pragma unroll
+        for (int j = 0; j < 8; j++) colbits[j] = rowmax[j] = all;
+    }
+    if (TILE) rows_out();
     if (p.qt) {
         // 8-byte slot g of column c sits at g ^ (c / 8): the 16 lanes of one g
         // then cover all banks, and a pair of slots stays one 16-byte chunk
@@ -158,11 +364,8 @@ __global__ __launch_bounds__(256) void quantize_kernel(QuantArgs p) {
 #pragma unroll
         for (int j = 0; j < 8; j++) {
             const int c = h * 8 + j;
-            const uint32_t b = scale_byte<FMT>(cmax[j]);
-            const float k = inverse_scale(b);
-            const uint32_t lo = codes4<FMT>(v[0][j] * k, v[1][j] * k, v[2][j] * k, v[3][j] * k);
-            const uint32_t hi = codes4<FMT>(v[4][j] * k, v[5][j] * k, v[6][j] * k, v[7][j] * k);
-            *(uint2_v*)(turned + c * kBlk + 8 * (g ^ h)) = uint2_v{lo, hi};
+            const uint32_t b = scale_byte<FMT>(float_bits<SQ, T>(colbits[j]));
+            *(uint2_v*)(turned + c * kBlk + 8 * (g ^ h)) = sq.template col_codes<FMT>(j, scale_of(b));
             if (g == 0 && c0 + j < p.cols) {
                 uint8_t* s = p.st + (uint64_t)(c0 + j) * p.s_pitch_t;
                 s[tr] = (uint8_t)b;

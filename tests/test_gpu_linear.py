@@ -303,7 +303,7 @@ def test_quantize_beyond_2_pow_32_bytes(torch):
 # ------------------------------------------------------------------ product --
 
 def workspace(torch, m, n, k):
-    need = L.demo_block_workspace(L.Product(), m, n, k)
+    need = max(L.demo_block_workspace(L.Product(), m, n, k, d) for d in (L.DTYPE_F32, L.DTYPE_BF16))
     return torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda") if need else None
 
 
@@ -494,7 +494,7 @@ class Layer:
         self.wq, self.wt = operand(torch, n, k), operand(torch, k, n)
         self.xq, self.xt = operand(torch, tokens, k), operand(torch, k, tokens)
         self.gq, self.gt = operand(torch, tokens, n), operand(torch, n, tokens)
-        need = max(L.demo_block_workspace(L.Product(), *s) for s in ((tokens, n, k), (tokens, k, n), (n, k, tokens)))
+        need = max(L.demo_block_workspace(L.Product(), *s, d) for d in (L.DTYPE_F32, L.DTYPE_BF16) for s in ((tokens, n, k), (tokens, k, n), (n, k, tokens)))
         self.ws = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
 
     def take_weight(self):

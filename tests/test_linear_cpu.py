@@ -139,7 +139,7 @@ def test_binding_refuses_host_tensors():
     x = torch.zeros(16, 128)
     u = torch.zeros(1 << 16, dtype=torch.uint8)
     for call in (lambda: L.demo_dropout(L.Dropout(), x, x.clone()), lambda: L.demo_dropout_backward(L.Dropout(), x, x),
-                 lambda: L.demo_block_quantize(L.Block(), x, u), lambda: L.demo_block_matmul(L.Product(), 16, 16, 16, u, u, x)):
+                 lambda: L.demo_block_quantize(L.Block(), x, u), lambda: L.demo_block_matmul(L.Product(), 16, 128, 16, u, u, x)):
         with pytest.raises(ValueError, match="device tensor"):
             call()
     with pytest.raises(TypeError, match="float32, float16 or bfloat16"):
