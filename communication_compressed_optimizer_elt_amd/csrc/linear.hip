@@ -127,11 +127,13 @@ struct Plan {
 //    2048: 32.2 against 38.3 us; 6144 x 4096 x 2048, where the second round is
 //    half empty: 56.3 against 53.9 us; 4096 x 2048 x 2048, half a round: 25.6
 //    against 19.9 us), so they are taken where rounds say so at 1.65;
-//  * up to 192 tiles of 128, tiles of 64 fill the card better (1024 x 2048 x
-//    2048: 9.8 against 15.6 us; 2048 x 2048 x 2048, 256 tiles: 17.0 against 15.8);
+//  * up to 256 tiles of 128, tiles of 64 fill the card better (1024 x 2048 x
+//    2048: 9.2 against 14.6 us; 2048 x 2048 x 2048, 256 tiles: 15.8 against 16.6
+//    us, 23.6 against 29.7 us with an fp32 result); with a sum of 8192 or more
+//    up to 192 (2048 x 2048 x 8192: 54 against 53 us, 85 against 79 us);
 //  * the sum is split where tiles fill less than a round: down to 16 blocks of
-//    128 for tiles of 64 (256 x 2048 x 8192: 17.4 us in 4, 24.0 in one; 128 x
-//    2048 x 2048: 8.1 us in one, 10.7 in 2), to 64 for tiles of 128 (2048 x 2048
+//    128 for tiles of 64 (256 x 2048 x 8192: 16.4 us in 4, 23.8 in one; 128 x
+//    2048 x 2048: 7.6 us in one, 9.7 in 2), to 64 for tiles of 128 (2048 x 2048
 //    x 16384: 80 us in 2, 90 in one).
 // fp32 results behave the same without the tiles of 256: what bounds them is
 // the bf16 instructions' power, not reading LDS (8192 x 8192 x 8192 at 1.24
@@ -143,7 +145,7 @@ Plan plan_of(uint64_t m, uint64_t n, uint64_t k, bool wide) {
     const auto rounds = [](uint64_t count, uint64_t at_once) { return (count + at_once - 1) / at_once; };
     if (!wide && m >= 256 && n >= 256 && 33 * rounds(tiles(256), 256) <= 20 * rounds(tiles(128), 512))
         return {256, 1, (uint32_t)up(kb, 4)};
-    const uint64_t tile = tiles(128) > 192 ? 128 : 64, least = tile == 128 ? 64 : 16;
+    const uint64_t tile = tiles(128) > (kb >= 64 ? 192u : 256u) ? 128 : 64, least = tile == 128 ? 64 : 16;
     uint64_t splits = 512 / tiles(tile);
     if (splits > kb / least) splits = kb / least;
     if (splits < 1) splits = 1;
@@ -153,10 +155,10 @@ Plan plan_of(uint64_t m, uint64_t n, uint64_t k, bool wide) {
 // the partial sums of up to 512 tiles of 128 x 128
 static_assert(512 * 128 * 128 * 4 <= DEMO_BLOCK_MAX_WORKSPACE, "workspace");
 
-template <int FA, int FB, bool WIDE, int TILE, int STAGES>
+template <int FA, int FB, bool WIDE, int TILE>
 hipError_t launch_tiles(const demo::ProductArgs& a, dim3 grid, hipStream_t s) {
-    return launch(demo::product_kernel<FA, FB, WIDE, TILE, TILE, 2, 2, STAGES>, grid, dim3(256),
-                  STAGES * 2 * TILE * DEMO_BLOCK + 2 * 2 * TILE * 4, s, a);
+    return launch(demo::product_kernel<FA, FB, WIDE, TILE, TILE, 2, 2>, grid, dim3(256),
+                  2 * 2 * TILE * (DEMO_BLOCK + 4), s, a);
 }
 
 template <int FA, int FB, bool WIDE>
@@ -172,8 +174,8 @@ hipError_t launch_product(demo::ProductArgs a, const Plan& plan, void* workspace
     a.tiles_n = (a.n + plan.tile - 1) / plan.tile;
     const dim3 grid(a.tiles_m * a.tiles_n, plan.splits);
     hipError_t e;
-    if (plan.tile == 64) e = launch_tiles<FA, FB, WIDE, 64, 4>(a, grid, s);
-    else if (WIDE || plan.tile == 128) e = launch_tiles<FA, FB, WIDE, 128, 2>(a, grid, s);
+    if (plan.tile == 64) e = launch_tiles<FA, FB, WIDE, 64>(a, grid, s);
+    else if (WIDE || plan.tile == 128) e = launch_tiles<FA, FB, WIDE, 128>(a, grid, s);
     else e = launch(demo::product_big_kernel<FA, FB>, grid, dim3(256), demo::kBigLds, s, a);
     if (e != hipSuccess || plan.splits == 1) return e;
     const uint64_t blocks = ((uint64_t)a.m * ((a.n + 7) / 8) + 255) / 256;

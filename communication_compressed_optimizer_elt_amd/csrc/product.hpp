@@ -281,20 +281,24 @@ __device__ __forceinline__ void sync_loads() {
 }
 
 // BM x BN of C by WM x WN waves, one of the splits of the sum (grid y).  LDS
-// holds STAGES blocks of 128 along the sum, filled by loads that go from memory
-// to LDS STAGES - 1 blocks ahead; one barrier a block.  Row r's 16-byte chunk c sits at c ^ (r / 2 & 7),
+// holds two blocks of 128 along the sum, filled by loads that go from memory to
+// LDS one block ahead; one barrier a block.  What hides the waits is a second
+// workgroup on the CU (four of 64 x 64): three or four stages, and with them
+// fewer workgroups, measured slower (2048 x 2048 x 2048 in tiles of 64: 15.8
+// us, 19.2 and 18.2 with three and four; 4096 x 8192 x 2048 in tiles of 128:
+// 71 us, 112 with four), and so did 8 waves of half the size (17.6 us).  Row r's 16-byte chunk c sits at c ^ (r / 2 & 7),
 // which spreads 16 rows' reads of one chunk over all 64 banks; loads into LDS
 // write lanes in order, so the exchange is made on their source addresses.
 // Rows past the matrix repeat its last row; what they give is not stored.
-template <int FA, int FB, bool WIDE, int BM, int BN, int WM, int WN, int STAGES>
+template <int FA, int FB, bool WIDE, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN) void product_kernel(ProductArgs p) {
     constexpr int NW = WM * WN, SM = BM / WM / 16, SN = BN / WN / 16;
     constexpr int LA = BM / 8 / NW, LB = BN / 8 / NW;
     constexpr int kStage = (BM + BN) * kBlkK, kScales = (BM + BN) * 4;
     static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0 && BM % 64 == 0 && BN % 64 == 0 && (BM + BN) / 64 <= NW, "loads per wave");
-    static_assert(NW * finish_bytes<SM, SN>() <= STAGES * kStage, "the way out fits the stages");
+    static_assert(NW * finish_bytes<SM, SN>() <= 2 * kStage, "the way out fits the stages");
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-    const uint8_t* scales = lds + STAGES * kStage;
+    const uint8_t* scales = lds + 2 * kStage;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     uint32_t tm, tn;
     tile_of(p, blockIdx.x, tm, tn);
@@ -324,29 +328,25 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(ProductArgs p) {
     const uint32_t os = srow * p.s_pitch;
 
     auto fetch = [&](uint32_t kb) {
-        const uint32_t at = lds0 + (kb - kb0) % STAGES * kStage;
+        const uint32_t at = lds0 + (kb & 1) * kStage;
 #pragma unroll
         for (int i = 0; i < LA; i++) load_lds16(ga + kb * kBlkK, oa[i], at + (wave + i * NW) * 1024);
 #pragma unroll
         for (int i = 0; i < LB; i++) load_lds16(gb + kb * kBlkK, ob[i], at + BM * kBlkK + (wave + i * NW) * 1024);
         if ((kb & 3) == 0 && wave < (BM + BN) / 64)  // four blocks' scale bytes
-            load_lds4(gs + kb, os, lds0 + STAGES * kStage + (kb >> 2 & 1) * kScales + wave * 256);
+            load_lds4(gs + kb, os, lds0 + 2 * kStage + (kb >> 2 & 1) * kScales + wave * 256);
     };
 
     const int wm = wave % WM, wn = wave / WM, row = lane & 15, g = lane >> 4;
     const int c0 = ((2 * g) ^ (row >> 1)) * 16, c1 = ((2 * g + 1) ^ (row >> 1)) * 16;
     v4f acc[SM][SN] = {};
     uint32_t ea[SM], eb[SN];
-#pragma unroll
-    for (int s = 0; s < STAGES - 1; s++)
-        if (kb0 + s < kb1) fetch(kb0 + s);
+    fetch(kb0);
     for (uint32_t kb = kb0; kb < kb1; kb++) {
-        // block kb has landed, and everyone has read the stage that is filled
-        // next.  A wave that loads scale bytes too waits for one load more.
-        if (kb + STAGES - 2 < kb1) sync_loads<(STAGES - 2) * (LA + LB)>();
-        else sync_loads<0>();
-        if (kb + STAGES - 1 < kb1) fetch(kb + STAGES - 1);
-        const uint8_t* stage = lds + (kb - kb0) % STAGES * kStage;
+        // block kb has landed, and everyone has read the stage that is filled next
+        sync_loads<0>();
+        if (kb + 1 < kb1) fetch(kb + 1);
+        const uint8_t* stage = lds + (kb & 1) * kStage;
         if ((kb & 3) == 0) {
             const uint32_t* sc = (const uint32_t*)(scales + (kb >> 2 & 1) * kScales);
 #pragma unroll

@@ -233,7 +233,7 @@ struct Square<float> : FloatSquare {};
 template <typename T>
 __device__ __forceinline__ void load_row(const T* src, bool wide, uint32_t left, uint32_t (&v)[4]) {
     if (wide) {
-        const uint4_v w = *(const uint4_v*)src;
+        const uint4_v w = __builtin_nontemporal_load((const uint4_v*)src);
 #pragma unroll
         for (int j = 0; j < 4; j++) v[j] = w[j];
     } else {
@@ -245,7 +245,10 @@ __device__ __forceinline__ void load_row(const T* src, bool wide, uint32_t left,
 }
 __device__ __forceinline__ void load_row(const float* src, bool wide, uint32_t left, float (&v)[8]) {
     if (wide) {
-        load8(src, v);
+        const float4_v a = __builtin_nontemporal_load((const float4_v*)src);
+        const float4_v b = __builtin_nontemporal_load((const float4_v*)(src + 4));
+#pragma unroll
+        for (int j = 0; j < 4; j++) v[j] = a[j], v[4 + j] = b[j];
     } else {
 #pragma unroll
         for (int j = 0; j < 8; j++)

@@ -357,9 +357,10 @@ def test_product(torch, m, n, k, out):
 
 @pytest.mark.parametrize("m,n,k,out,fa,fb", [
     (2000, 8000, 128, "bf16", 0, 0), (2000, 8000, 300, "f16", 1, 0), (1999, 8000, 385, "bf16", 0, 1), (2048, 8192, 520, "bf16", 1, 1),
-    (1801, 7944, 700, "f16", 0, 0), (2000, 8001, 900, "bf16", 0, 0), (1793, 7937, 1100, "f16", 0, 0), (2040, 8184, 2000, "bf16", 0, 0)])
+    (1801, 7944, 700, "f16", 0, 0), (2000, 8001, 900, "bf16", 0, 0), (1793, 7937, 1100, "f16", 0, 0), (2040, 8184, 2000, "bf16", 0, 0),
+    (1000, 5000, 300, "bf16", 0, 0), (1000, 5001, 640, "f16", 1, 1), (1000, 5000, 300, "f32", 1, 0), (2000, 4001, 700, "f32", 0, 0)])
 def test_product_large_tiles(torch, m, n, k, out, fa, fb):
-    """Sizes of the 256 x 256 tiles, whole and moved back at the ends, sums of 1 to 16 blocks."""
+    """Sizes of the 256 x 256 tiles, whole and moved back at the ends, sums of 1 to 16 blocks; and of the 128 x 128 tiles."""
     a, va, b, vb = operands(torch, m, n, k, fa, fb, spread=2)
     c = torch.full((m, n), float("nan"), dtype=dt(torch, out), device="cuda")
     cfg = L.Product(fmt_a=fa, fmt_b=fb)
@@ -467,6 +468,15 @@ def test_product_is_the_same_every_time(torch):
         for x in c:
             L.demo_block_matmul(L.Product(), m, n, k, a, b, x, workspace=ws)
         assert torch.equal(c[0], c[1]) and torch.equal(c[0], c[2])
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_product_split_sum_of_large_tiles(torch, out):
+    m, n, k = 1800, 1900, 16500
+    a, va, b, vb = operands(torch, m, n, k, spread=1)
+    c = torch.empty(m, n, dtype=dt(torch, out), device="cuda")
+    L.demo_block_matmul(L.Product(), m, n, k, a, b, c, workspace=workspace(torch, m, n, k))
+    check_product(torch, c, va, vb)
 
 
 def test_product_long_sum(torch):
