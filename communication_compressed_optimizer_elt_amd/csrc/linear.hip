@@ -135,15 +135,14 @@ struct Plan {
 //    128 for tiles of 64 (256 x 2048 x 8192: 16.4 us in 4, 23.8 in one; 128 x
 //    2048 x 2048: 7.6 us in one, 9.7 in 2), to 64 for tiles of 128 (2048 x 2048
 //    x 16384: 80 us in 2, 90 in one).
-// fp32 results behave the same without the tiles of 256: what bounds them is
-// the bf16 instructions' power, not reading LDS (8192 x 8192 x 8192 at 1.24
-// PFLOP/s in tiles of 128, 1.26 in tiles of 256).
+// With an fp32 result a round of 256 tiles costs 1.75 to 1.87 of 128 (8192 x
+// 8192 x 8192: 890 against 969 us; 4096 x 8192 x 2048: 148 against 158 us).
 Plan plan_of(uint64_t m, uint64_t n, uint64_t k, bool wide) {
     const uint64_t kb = up(k, DEMO_BLOCK) / DEMO_BLOCK;
     if (m <= kFewRows) return {0, 1, (uint32_t)kb};
     const auto tiles = [&](uint64_t t) { return up(m, t) / t * (up(n, t) / t); };
     const auto rounds = [](uint64_t count, uint64_t at_once) { return (count + at_once - 1) / at_once; };
-    if (!wide && m >= 256 && n >= 256 && 33 * rounds(tiles(256), 256) <= 20 * rounds(tiles(128), 512))
+    if (m >= 256 && n >= 256 && (wide ? 37 : 33) * rounds(tiles(256), 256) <= 20 * rounds(tiles(128), 512))
         return {256, 1, (uint32_t)up(kb, 4)};
     const uint64_t tile = tiles(128) > (kb >= 64 ? 192u : 256u) ? 128 : 64, least = tile == 128 ? 64 : 16;
     uint64_t splits = 512 / tiles(tile);
@@ -175,7 +174,8 @@ hipError_t launch_product(demo::ProductArgs a, const Plan& plan, void* workspace
     const dim3 grid(a.tiles_m * a.tiles_n, plan.splits);
     hipError_t e;
     if (plan.tile == 64) e = launch_tiles<FA, FB, WIDE, 64>(a, grid, s);
-    else if (WIDE || plan.tile == 128) e = launch_tiles<FA, FB, WIDE, 128>(a, grid, s);
+    else if (plan.tile == 128) e = launch_tiles<FA, FB, WIDE, 128>(a, grid, s);
+    else if (WIDE) e = launch(demo::product_big_wide_kernel<FA, FB>, grid, dim3(512), demo::kBigLds, s, a);
     else e = launch(demo::product_big_kernel<FA, FB>, grid, dim3(256), demo::kBigLds, s, a);
     if (e != hipSuccess || plan.splits == 1) return e;
     const uint64_t blocks = ((uint64_t)a.m * ((a.n + 7) / 8) + 255) / 256;

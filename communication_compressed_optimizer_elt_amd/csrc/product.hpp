@@ -10,11 +10,13 @@
 //    eight products of each 8 neighbouring values of the sum at the largest of
 //    them and keep 13 binary places below it.  On random data that is 1.4e-5 of the result,
 //    a hundredth of the rounding of a 16-bit result, so 16-bit results take it;
-//  * bf16 matrix instructions (2.48 PFLOP/s from registers) on codes widened
+//  * bf16 matrix instructions (2.38 PFLOP/s from registers) on codes widened
 //    to bf16 with their scale, which is exact, and whose products and sums are
 //    those of fp32: fp32 results take it (WIDE).  A code times its scale has to
 //    stay below 2^128, bf16's range.
 #pragma once
+
+#include <type_traits>
 
 #include "dropout.hpp"
 
@@ -97,8 +99,11 @@ struct Row8 {
 };
 
 // The same for P rows at once, in aligned accesses: every load of the addend
-// is in flight before the first sum, every store behind the last.  on[r]: the
-// row and its eight columns are this tile's to write.
+// is in flight before the first sum, every store behind the last.  16-bit rows
+// go past the caches (logits of 2048 tokens: 368 us, 421 us through them);
+// fp32 rows, 16 bytes of every 32 at a time, do not (2048 x 8192 x 8192: 254
+// us, 266 us past them).  on[r]: the row and its eight columns are this tile's
+// to write.
 template <typename T, int P>
 __device__ __forceinline__ void finish_rows(const ProductArgs& p, const uint64_t (&i)[P], uint32_t j, const bool (&on)[P],
                                             float (&v)[P][8]) {
@@ -117,7 +122,10 @@ __device__ __forceinline__ void finish_rows(const ProductArgs& p, const uint64_t
     }
 #pragma unroll
     for (int r = 0; r < P; r++)
-        if (on[r]) stream8((T*)p.c + i[r] * p.ldc + j, v[r]);
+        if (on[r]) {
+            if constexpr (sizeof(T) == 2) stream8((T*)p.c + i[r] * p.ldc + j, v[r]);
+            else store8((T*)p.c + i[r] * p.ldc + j, v[r]);
+        }
 }
 
 // A wave's SM x SN accumulators of 16 x 16 (lane l holds row l % 16, columns 4
@@ -129,25 +137,36 @@ __device__ __forceinline__ void finish_rows(const ProductArgs& p, const uint64_t
 template <int SM, int SN>
 constexpr int finish_bytes() { return 16 * (SM < 2 ? 1 : 2) * (SN * 16 + 4) * 4; }
 
-template <int SM, int SN>
-__device__ __forceinline__ void finish(const ProductArgs& p, const v4f (&acc)[SM][SN], float* slab, uint32_t i0,
-                                       uint32_t j0, uint32_t lo_i, uint32_t lo_j, int lane) {
-    constexpr int H = SM < 2 ? 1 : 2, kRow = SN * 16 + 4, kLanes = SN * 2, kRows = 64 / kLanes, P = 16 * H / kRows;
-    static_assert(SM % H == 0 && P >= 1, "whole slabs");
+template <int N>
+using Int = std::integral_constant<int, N>;
+
+// f(Int<s>()) of a run-time s < N: registers have no index.  The branches are
+// told apart at their ends, or the compiler would make one of them that finds
+// the accumulators in memory.
+template <int N, int T = 0, typename F>
+__device__ __forceinline__ void pick(int s, F f) {
+    if constexpr (T < N) {
+        if (s == T) {
+            f(Int<T>());
+            asm volatile("; %0" ::"n"(T));
+        } else {
+            pick<N, T + 1>(s, f);
+        }
+    }
+}
+
+// S pieces of 16 H rows x 16 SN columns; write(Int<t>()) puts piece t into the
+// slab.
+template <int S, int H, int SN, typename F>
+__device__ __forceinline__ void finish_pieces(const ProductArgs& p, float* slab, uint32_t i0, uint32_t j0, uint32_t lo_i,
+                                              uint32_t lo_j, int lane, F write) {
+    constexpr int kRow = SN * 16 + 4, kLanes = SN * 2, kRows = 64 / kLanes, P = 16 * H / kRows;
+    static_assert(P >= 1, "a pass fits a piece");
     const uint32_t j = j0 + lane % kLanes * 8;
-    const bool col = j >= lo_j && j < p.n;
+    const bool col = j + 8 > lo_j && j < p.n;
 #pragma unroll 1
-    for (int s = 0; s < SM / H; s++) {
-        // registers have no index: one branch a slab (uniform)
-#pragma unroll
-        for (int t = 0; t < SM / H; t++)
-            if (s == t) {
-#pragma unroll
-                for (int i = 0; i < H; i++)
-#pragma unroll
-                    for (int c = 0; c < SN; c++)
-                        *(v4f*)(slab + (i * 16 + (lane & 15)) * kRow + c * 16 + 4 * (lane >> 4)) = acc[t * H + i][c];
-            }
+    for (int s = 0; s < S; s++) {
+        pick<S>(s, write);
         wave_lds_sync();
         const uint32_t top = i0 + s * 16 * H;
         if (p.wide) {
@@ -178,6 +197,21 @@ __device__ __forceinline__ void finish(const ProductArgs& p, const v4f (&acc)[SM
         }
         wave_lds_sync();
     }
+}
+
+template <int SM, int SN>
+__device__ __forceinline__ void finish(const ProductArgs& p, const v4f (&acc)[SM][SN], float* slab, uint32_t i0,
+                                       uint32_t j0, uint32_t lo_i, uint32_t lo_j, int lane) {
+    constexpr int H = SM < 2 ? 1 : 2, kRow = SN * 16 + 4;
+    static_assert(SM % H == 0, "whole pieces");
+    finish_pieces<SM / H, H, SN>(p, slab, i0, j0, lo_i, lo_j, lane, [&](auto T) {
+        constexpr int t = decltype(T)::value;
+#pragma unroll
+        for (int i = 0; i < H; i++)
+#pragma unroll
+            for (int c = 0; c < SN; c++)
+                *(v4f*)(slab + (i * 16 + (lane & 15)) * kRow + c * 16 + 4 * (lane >> 4)) = acc[t * H + i][c];
+    });
 }
 
 typedef __bf16 v8b __attribute__((ext_vector_type(8)));

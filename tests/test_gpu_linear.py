@@ -358,7 +358,8 @@ def test_product(torch, m, n, k, out):
 @pytest.mark.parametrize("m,n,k,out,fa,fb", [
     (2000, 8000, 128, "bf16", 0, 0), (2000, 8000, 300, "f16", 1, 0), (1999, 8000, 385, "bf16", 0, 1), (2048, 8192, 520, "bf16", 1, 1),
     (1801, 7944, 700, "f16", 0, 0), (2000, 8001, 900, "bf16", 0, 0), (1793, 7937, 1100, "f16", 0, 0), (2040, 8184, 2000, "bf16", 0, 0),
-    (1000, 5000, 300, "bf16", 0, 0), (1000, 5001, 640, "f16", 1, 1), (1000, 5000, 300, "f32", 1, 0), (2000, 4001, 700, "f32", 0, 0)])
+    (1000, 5000, 300, "bf16", 0, 0), (1000, 5001, 640, "f16", 1, 1), (1000, 5000, 300, "f32", 1, 0), (2000, 4001, 700, "f32", 0, 0),
+    (2000, 8000, 128, "f32", 0, 1), (1999, 8001, 300, "f32", 1, 0), (2040, 8184, 1100, "f32", 1, 1), (1801, 7944, 520, "f32", 0, 0)])
 def test_product_large_tiles(torch, m, n, k, out, fa, fb):
     """Sizes of the 256 x 256 tiles, whole and moved back at the ends, sums of 1 to 16 blocks; and of the 128 x 128 tiles."""
     a, va, b, vb = operands(torch, m, n, k, fa, fb, spread=2)
