@@ -31,15 +31,20 @@ __device__ __forceinline__ void draw_block(const Drop& d, uint64_t blk, uint32_t
     philox4x32_10((uint32_t)blk, (uint32_t)(blk >> 32), d.step, d.c3, d.k0, d.k1, w);
 }
 
-// v[j] = element j of Philox block `blk` is kept ? v[j] * scale : 0
-__device__ __forceinline__ void drop_block(const Drop& d, uint64_t blk, float (&v)[8]) {
-    uint32_t w[4];
-    draw_block(d, blk, w);
+// v[j] = v[j] * scale where the block's draw keeps it, else 0
+__device__ __forceinline__ void drop_drawn(const Drop& d, const uint32_t (&w)[4], float (&v)[8]) {
 #pragma unroll
     for (int j = 0; j < 4; j++) {
         v[2 * j] = (w[j] & 0xFFFFu) >= d.threshold ? v[2 * j] * d.scale : 0.f;
         v[2 * j + 1] = (w[j] >> 16) >= d.threshold ? v[2 * j + 1] * d.scale : 0.f;
     }
+}
+
+// v[j] = element j of Philox block `blk` is kept ? v[j] * scale : 0
+__device__ __forceinline__ void drop_block(const Drop& d, uint64_t blk, float (&v)[8]) {
+    uint32_t w[4];
+    draw_block(d, blk, w);
+    drop_drawn(d, w, v);
 }
 
 // the same for elements e + j, e counted from the tensor's element 0: they

@@ -86,19 +86,23 @@ int dropout_impl(const demo_dropout_cfg* cfg, uint32_t dtype, uint64_t n, const 
     }
 }
 
-template <typename T, int FMT>
-hipError_t launch_quantize(const demo::QuantArgs& a, bool tile, dim3 grid, hipStream_t s) {
+template <typename T, int FMT, bool TILE>
+hipError_t launch_quantize(const demo::QuantArgs& a, bool wide, dim3 grid, hipStream_t s) {
     if (a.drop.on)
-        return launch(tile ? demo::quantize_kernel<T, FMT, true, true> : demo::quantize_kernel<T, FMT, false, true>, grid,
-                      dim3(256), 0, s, a);
-    return launch(tile ? demo::quantize_kernel<T, FMT, true, false> : demo::quantize_kernel<T, FMT, false, false>, grid,
-                  dim3(256), 0, s, a);
+        return launch(wide ? demo::quantize_kernel<T, FMT, TILE, true, true> : demo::quantize_kernel<T, FMT, TILE, true, false>,
+                      grid, dim3(256), 0, s, a);
+    return launch(wide ? demo::quantize_kernel<T, FMT, TILE, false, true> : demo::quantize_kernel<T, FMT, TILE, false, false>,
+                  grid, dim3(256), 0, s, a);
 }
 
 template <typename T>
 hipError_t launch_quantize(const demo::QuantArgs& a, const demo_block_cfg* cfg, dim3 grid, hipStream_t s) {
-    return cfg->fmt == DEMO_FMT_E4M3 ? launch_quantize<T, demo::kE4M3>(a, cfg->tile != 0, grid, s)
-                                     : launch_quantize<T, demo::kE5M2>(a, cfg->tile != 0, grid, s);
+    const bool wide = aligned16(a.src) && a.ld * sizeof(T) % 16 == 0 && a.cols % 8 == 0;
+    if (cfg->fmt == DEMO_FMT_E4M3)
+        return cfg->tile ? launch_quantize<T, demo::kE4M3, true>(a, wide, grid, s)
+                         : launch_quantize<T, demo::kE4M3, false>(a, wide, grid, s);
+    return cfg->tile ? launch_quantize<T, demo::kE5M2, true>(a, wide, grid, s)
+                     : launch_quantize<T, demo::kE5M2, false>(a, wide, grid, s);
 }
 
 int check_product(const demo_product_cfg* cfg, uint64_t m, uint64_t n, uint64_t k) {
@@ -242,7 +246,6 @@ int demo_block_quantize(const demo_block_cfg* cfg, uint64_t rows, uint64_t cols,
         a.s_pitch_t = (uint32_t)t.scale_pitch;
     }
     a.tiles_c = (uint32_t)(o.pitch / DEMO_BLOCK);
-    a.wide = aligned16(src) && ld * eb % 16 == 0 && cols % 8 == 0;
     const dim3 grid(a.tiles_c * (uint32_t)((rows + DEMO_BLOCK - 1) / DEMO_BLOCK));
     hipStream_t s = static_cast<hipStream_t>(hip_stream);
     switch (cfg->dtype) {

@@ -1,10 +1,12 @@
-// number.hpp -- the storage types of the linear-layer operators (fp32, fp16,
-// bf16, 8-bit e4m3 and e5m2) and their conversions.  Every rounding is to
-// nearest even, by the hardware's conversions.
+// number.hpp -- what the linear-layer operators share: the storage types (fp32,
+// fp16, bf16, 8-bit e4m3 and e5m2) with their conversions, which round to
+// nearest even by the hardware's instructions, and the order of tiles.
 #pragma once
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include "device_common.hpp"
 
 namespace demo {
 
@@ -78,6 +80,21 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
         w = __builtin_amdgcn_cvt_pk_bf8_f32(c, d, w, true);
     }
     return (uint32_t)w;
+}
+
+// Tile of workgroup `id`: the 8 XCDs, which take ids in turn, get runs of
+// neighbouring tiles each, and a run goes down kTileRun row tiles before it
+// takes the next column tile, so that one XCD's workgroups share rows of both
+// operands of a product in its L2, and the pieces of a transposed row that
+// they write lie side by side.
+constexpr uint32_t kTileRun = 8;
+
+__device__ __forceinline__ void tile_of(uint32_t tiles_m, uint32_t tiles_n, uint32_t id, uint32_t& tm, uint32_t& tn) {
+    const uint32_t tiles = tiles_m * tiles_n, q = tiles / kXcds, r = tiles % kXcds, x = id % kXcds;
+    id = x * q + min(x, r) + id / kXcds;
+    const uint32_t band = kTileRun * tiles_n, first = id / band * kTileRun, high = min(tiles_m - first, kTileRun);
+    tm = first + id % band % high;
+    tn = id % band / high;
 }
 
 }  // namespace demo

@@ -291,20 +291,6 @@ __device__ __forceinline__ ProductArgs target(const ProductArgs& p, uint32_t spl
     return t;
 }
 
-// Tile of workgroup `id`: the 8 XCDs, which take ids in turn, get runs of
-// neighbouring tiles each, and a run goes down kTileRun row tiles before it
-// takes the next column tile, so that one XCD's workgroups share rows of both
-// operands in its L2.
-constexpr uint32_t kTileRun = 8;
-
-__device__ __forceinline__ void tile_of(const ProductArgs& p, uint32_t id, uint32_t& tm, uint32_t& tn) {
-    const uint32_t tiles = p.tiles_m * p.tiles_n, q = tiles / kXcds, r = tiles % kXcds, x = id % kXcds;
-    id = x * q + min(x, r) + id / kXcds;
-    const uint32_t band = kTileRun * p.tiles_n, first = id / band * kTileRun, high = min(p.tiles_m - first, kTileRun);
-    tm = first + id % band % high;
-    tn = id % band / high;
-}
-
 // All but the N newest of this wave's loads have landed and its LDS reads are
 // done; then the same holds for every wave.
 template <int N>
@@ -335,7 +321,7 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(ProductArgs p) {
     const uint8_t* scales = lds + 2 * kStage;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     uint32_t tm, tn;
-    tile_of(p, blockIdx.x, tm, tn);
+    tile_of(p.tiles_m, p.tiles_n, blockIdx.x, tm, tn);
     const uint32_t m0 = tm * BM, n0 = tn * BN;
     const uint32_t kb0 = blockIdx.y * p.kb_split, kb1 = min(kb0 + p.kb_split, p.kb);
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane(

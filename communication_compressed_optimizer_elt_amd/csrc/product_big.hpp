@@ -51,7 +51,7 @@ __device__ __forceinline__ BigTile big_tile(const ProductArgs& p, uint8_t* lds) 
     t.lane = threadIdx.x & 63;
     t.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     uint32_t tm, tn;
-    tile_of(p, blockIdx.x, tm, tn);
+    tile_of(p.tiles_m, p.tiles_n, blockIdx.x, tm, tn);
     t.lo_i = tm * kBig;
     t.lo_j = tn * kBig;
     t.m0 = min(t.lo_i, p.m - kBig);
@@ -268,7 +268,7 @@ __global__ __launch_bounds__(512, 2) void product_big_wide_kernel(ProductArgs p)
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     uint32_t tm, tn;
-    tile_of(p, blockIdx.x, tm, tn);
+    tile_of(p.tiles_m, p.tiles_n, blockIdx.x, tm, tn);
     const uint32_t lo_i = tm * kBig, lo_j = tn * kBig, m0 = min(lo_i, p.m - kBig), n0 = min(lo_j, p.n - kBig);
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane(
         (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds);

@@ -11,7 +11,17 @@
 // work-item t holds rows 8 (t / 16) .. +7 of columns 8 (t % 16) .. +7, so eight
 // codes in a row make one 8-byte store of the row operand and eight codes in
 // a column one 8-byte LDS store of the transposed one.  The square's maxima go
-// through 16-lane exchanges (rows) and a small LDS table (columns).
+// through 16-lane exchanges (rows) and a small LDS table (columns); 16-bit
+// sources stay pairs of 16 bits, whose magnitudes compare as integers, until
+// the hardware's scaled conversion makes codes of them.
+//
+// Bound by memory: 16384 x 8192 bf16 to e4m3, both operands (537 MB), takes 99
+// us (5.4 TB/s; 112 us before the pieces of a transposed row were written side
+// by side and the source read past the caches); 8192 x 2048 fp32 in squares
+// (101 MB) 24 us and 16384 x 2048 bf16 through a dropout to e5m2 (134 MB) 35 us,
+// one or two rounds of workgroups whose loads, arithmetic and stores coincide.
+// Workgroups that stay and load their next square early spilled and took twice
+// as long (54 us for the fp32 weight).
 #pragma once
 
 #include <type_traits>
@@ -33,7 +43,6 @@ struct QuantArgs {
     uint64_t pitch_t;
     uint32_t s_pitch_t;
     uint32_t tiles_c;     // column tiles
-    uint32_t wide;        // rows of src are 16-byte aligned and cols a multiple of 8
     Drop drop;
 };
 
@@ -229,31 +238,31 @@ struct Square : PairSquare<T> {};
 template <>
 struct Square<float> : FloatSquare {};
 
-// Eight neighbours of a row from 0-bits on: pairs or floats
+// Eight neighbours of a row, as pairs or floats: in 16-byte loads past the
+// caches (the source is read once), or the first `left` one by one into zeros
 template <typename T>
-__device__ __forceinline__ void load_row(const T* src, bool wide, uint32_t left, uint32_t (&v)[4]) {
-    if (wide) {
-        const uint4_v w = __builtin_nontemporal_load((const uint4_v*)src);
+__device__ __forceinline__ void load_wide(const T* src, uint32_t (&v)[4]) {
+    const uint4_v w = __builtin_nontemporal_load((const uint4_v*)src);
 #pragma unroll
-        for (int j = 0; j < 4; j++) v[j] = w[j];
-    } else {
-        const uint16_t* s = (const uint16_t*)src;
-#pragma unroll
-        for (int j = 0; j < 8; j++)
-            if ((uint32_t)j < left) v[j >> 1] |= (uint32_t)s[j] << 16 * (j & 1);
-    }
+    for (int j = 0; j < 4; j++) v[j] = w[j];
 }
-__device__ __forceinline__ void load_row(const float* src, bool wide, uint32_t left, float (&v)[8]) {
-    if (wide) {
-        const float4_v a = __builtin_nontemporal_load((const float4_v*)src);
-        const float4_v b = __builtin_nontemporal_load((const float4_v*)(src + 4));
+__device__ __forceinline__ void load_wide(const float* src, float (&v)[8]) {
+    const float4_v a = __builtin_nontemporal_load((const float4_v*)src);
+    const float4_v b = __builtin_nontemporal_load((const float4_v*)(src + 4));
 #pragma unroll
-        for (int j = 0; j < 4; j++) v[j] = a[j], v[4 + j] = b[j];
-    } else {
+    for (int j = 0; j < 4; j++) v[j] = a[j], v[4 + j] = b[j];
+}
+template <typename T>
+__device__ __forceinline__ void load_each(const T* src, uint32_t left, uint32_t (&v)[4]) {
+    const uint16_t* s = (const uint16_t*)src;
 #pragma unroll
-        for (int j = 0; j < 8; j++)
-            if ((uint32_t)j < left) v[j] = src[j];
-    }
+    for (int j = 0; j < 8; j++)
+        if ((uint32_t)j < left) v[j >> 1] |= (uint32_t)s[j] << 16 * (j & 1);
+}
+__device__ __forceinline__ void load_each(const float* src, uint32_t left, float (&v)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; j++)
+        if ((uint32_t)j < left) v[j] = src[j];
 }
 
 // fp32 bits of a maximum as the square keeps it
@@ -263,8 +272,9 @@ __device__ __forceinline__ uint32_t float_bits(uint32_t u) {
     else return u;
 }
 
-// DROP: the source through a dropout's gradient, as floats.
-template <typename T, int FMT, bool TILE, bool DROP>
+// DROP: the source through a dropout's gradient, as floats.  WIDE: rows of src
+// are 16-byte aligned and cols a multiple of 8.
+template <typename T, int FMT, bool TILE, bool DROP, bool WIDE>
 __global__ __launch_bounds__(256, 4) void quantize_kernel(QuantArgs p) {
     typedef typename std::conditional<DROP, FloatSquare, Square<T>>::type SQ;
     constexpr int kCols = SQ::kPacked ? 4 : 8;  // words of a work-item's columns' maxima
@@ -272,20 +282,42 @@ __global__ __launch_bounds__(256, 4) void quantize_kernel(QuantArgs p) {
     __shared__ __attribute__((aligned(16))) uint8_t turned[kBlk * kBlk];
     const int t = threadIdx.x, g = t >> 4, h = t & 15, wave = t >> 6;
     // neighbouring squares go to one XCD, whose L2 gathers their single scale bytes
-    const uint32_t q8 = gridDim.x / kXcds, r8 = gridDim.x % kXcds, x8 = blockIdx.x % kXcds;
-    const uint32_t id = x8 * q8 + min(x8, r8) + blockIdx.x / kXcds;
-    const uint32_t tc = id % p.tiles_c, tr = id / p.tiles_c;
+    const uint32_t tiles_r = (p.rows + kBlk - 1) / kBlk;
+    uint32_t tr, tc;
+    tile_of(tiles_r, p.tiles_c, blockIdx.x, tr, tc);
     const uint32_t r0 = tr * kBlk + g * 8, c0 = tc * kBlk + h * 8;
 
     SQ sq;
     {
+        constexpr int kWords = Square<T>::kPacked ? 4 : 8;
+        const T* src = (const T*)p.src;
         Square<T> raw;
+        if (WIDE) {
+            // what lies outside repeats the last row or columns, and becomes zero
+            const uint32_t c = min(c0, p.cols - 8);
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
+            for (int i = 0; i < 8; i++) load_wide(src + (uint64_t)min(r0 + i, p.rows - 1) * p.ld + c, raw.v[i]);
+        } else {
 #pragma unroll
-            for (int j = 0; j < (Square<T>::kPacked ? 4 : 8); j++) raw.v[i][j] = 0;
-            if (r0 + i < p.rows && c0 < p.cols)
-                load_row((const T*)p.src + (uint64_t)(r0 + i) * p.ld + c0, p.wide, p.cols - c0, raw.v[i]);
+            for (int i = 0; i < 8; i++) {
+#pragma unroll
+                for (int j = 0; j < kWords; j++) raw.v[i][j] = 0;
+                if (r0 + i < p.rows && c0 < p.cols) load_each(src + (uint64_t)(r0 + i) * p.ld + c0, p.cols - c0, raw.v[i]);
+            }
+        }
+        uint32_t drawn[8][4];
+        if (WIDE && DROP) {  // drawn while the loads are under way
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                draw_block(p.drop, p.drop.first + (((uint64_t)(r0 + i) * p.cols + c0) >> 3), drawn[i]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        if (WIDE && ((tr + 1) * kBlk > p.rows || (tc + 1) * kBlk > p.cols)) {
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+#pragma unroll
+                for (int j = 0; j < kWords; j++)
+                    if (r0 + i >= p.rows || c0 >= p.cols) raw.v[i][j] = 0;
         }
         if constexpr (!DROP) {
             static_cast<Square<T>&>(sq) = raw;
@@ -297,9 +329,8 @@ __global__ __launch_bounds__(256, 4) void quantize_kernel(QuantArgs p) {
                     if constexpr (Square<T>::kPacked) sq.v[i][j] = Square<T>::number(raw.v[i][j >> 1] >> 16 * (j & 1));
                     else sq.v[i][j] = raw.v[i][j];
                 }
-                const uint64_t e = (uint64_t)(r0 + i) * p.cols + c0;
-                if (p.cols % 8 == 0) drop_block(p.drop, p.drop.first + (e >> 3), sq.v[i]);
-                else drop8(p.drop, e, sq.v[i]);
+                if (WIDE) drop_drawn(p.drop, drawn[i], sq.v[i]);
+                else drop8(p.drop, (uint64_t)(r0 + i) * p.cols + c0, sq.v[i]);
             }
         }
     }
@@ -363,7 +394,6 @@ __global__ __launch_bounds__(256, 4) void quantize_kernel(QuantArgs p) {
     if (p.qt) {
         // 8-byte slot g of column c sits at g ^ (c / 8): the 16 lanes of one g
         // then cover all banks, and a pair of slots stays one 16-byte chunk
-        const uint32_t tiles_r = (p.rows + kBlk - 1) / kBlk;
 #pragma unroll
         for (int j = 0; j < 8; j++) {
             const int c = h * 8 + j;
