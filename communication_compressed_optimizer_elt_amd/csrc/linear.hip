@@ -29,6 +29,11 @@ bool sides_ok(uint64_t rows, uint64_t cols) {
     return rows >= 1 && cols >= 1 && rows <= kMaxSide && cols <= kMaxSide && rows * cols <= DEMO_MAX_ELEMS;
 }
 
+// a row pitch that keeps every index of the matrix in 64 bits with room to spare
+bool pitch_ok(uint64_t rows, uint64_t cols, uint64_t ld) {
+    return ld >= cols && ld <= DEMO_MAX_ELEMS && rows - 1 <= ((uint64_t)1 << 40) / ld;
+}
+
 demo_operand operand_of(uint64_t rows, uint64_t cols) {
     demo_operand o{};
     o.pitch = up(cols, DEMO_BLOCK);
@@ -115,7 +120,9 @@ int check_product(const demo_product_cfg* cfg, uint64_t m, uint64_t n, uint64_t 
     return DEMO_OK;
 }
 
-constexpr uint64_t kFewRows = 16;
+// the kernels for few rows, and the columns that their grids hold (below 2^32
+// work-items)
+constexpr uint64_t kFewRows = 16, kFewRowsMaxCols = (uint64_t)1 << 22;
 
 // How a product is cut: tiles of `tile` x `tile` and `splits` of the sum, or
 // (tile 0) the kernels for few rows.
@@ -143,7 +150,7 @@ struct Plan {
 // 8192 x 8192: 890 against 969 us; 4096 x 8192 x 2048: 148 against 158 us).
 Plan plan_of(uint64_t m, uint64_t n, uint64_t k, bool wide) {
     const uint64_t kb = up(k, DEMO_BLOCK) / DEMO_BLOCK;
-    if (m <= kFewRows) return {0, 1, (uint32_t)kb};
+    if (m <= kFewRows && n <= kFewRowsMaxCols) return {0, 1, (uint32_t)kb};
     const auto tiles = [&](uint64_t t) { return up(m, t) / t * (up(n, t) / t); };
     const auto rounds = [](uint64_t count, uint64_t at_once) { return (count + at_once - 1) / at_once; };
     if (m >= 256 && n >= 256 && (wide ? 37 : 33) * rounds(tiles(256), 256) <= 20 * rounds(tiles(128), 512))
@@ -218,7 +225,7 @@ int demo_block_quantize(const demo_block_cfg* cfg, uint64_t rows, uint64_t cols,
     if (!cfg) return DEMO_EINVAL;
     if (cfg->abi_version != DEMO_ABI_VERSION) return DEMO_EABI;
     if (cfg->fmt > DEMO_FMT_E5M2 || cfg->tile > 1 || cfg->dtype > DEMO_DTYPE_BF16) return DEMO_EINVAL;
-    if (!sides_ok(rows, cols) || ld < cols || ld > DEMO_MAX_ELEMS) return DEMO_EINVAL;
+    if (!sides_ok(rows, cols) || !pitch_ok(rows, cols, ld)) return DEMO_EINVAL;
     demo::QuantArgs a{};
     if (const int rc = drop_of(dropout, rows * cols, &a.drop)) return rc;
     if (!src || (!operand && !operand_t)) return DEMO_EINVAL;
@@ -267,8 +274,7 @@ int demo_block_matmul(const demo_product_cfg* cfg, uint64_t m, uint64_t n, uint6
                       void* c, uint64_t ldc, const void* addend, uint64_t ld_addend, const demo_dropout_cfg* dropout,
                       void* workspace, uint64_t workspace_bytes, void* hip_stream) {
     if (const int rc = check_product(cfg, m, n, k)) return rc;
-    if (ldc < n || ldc > DEMO_MAX_ELEMS) return DEMO_EINVAL;
-    if (addend && (ld_addend < n || ld_addend > DEMO_MAX_ELEMS)) return DEMO_EINVAL;
+    if (!pitch_ok(m, n, ldc) || (addend && !pitch_ok(m, n, ld_addend))) return DEMO_EINVAL;
     demo::ProductArgs p{};
     if (const int rc = drop_of(dropout, m * n, &p.drop)) return rc;
     if (!a || !b || !c) return DEMO_EINVAL;

@@ -319,10 +319,10 @@ int demo_dropout_backward(const demo_dropout_cfg *cfg, uint32_t dtype, uint64_t 
 int demo_block_layout(uint64_t rows, uint64_t cols, demo_operand *out);
 
 /*
- * Quantises src [rows][cols] (row pitch ld elements, aligned to its element)
- * into operand (rows x cols, blocks along the columns) and into operand_t
- * (cols x rows: the transposed matrix, blocks along the rows) in one pass;
- * one of the two may be NULL.  A block's scale is 2^e with the smallest e >=
+ * Quantises src [rows][cols] (row pitch ld elements, (rows - 1)*ld at most
+ * 2^40, aligned to its element) into operand (rows x cols, blocks along the
+ * columns) and into operand_t (cols x rows: the transposed matrix, blocks along
+ * the rows) in one pass; one of the two may be NULL.  A block's scale is 2^e with the smallest e >=
  * -127 that keeps its largest finite magnitude within the format; codes are
  * rounded to nearest even; infinities and NaN become NaN codes.  With dropout
  * the values are first multiplied as demo_dropout_backward does (element i =
@@ -342,13 +342,19 @@ int demo_block_workspace(const demo_product_cfg *cfg, uint64_t m, uint64_t n, ui
  *   dX = product of dY's operand and W's operand_t,
  *   dW = product of dY's operand_t and X's operand_t.
  * Sums are held in fp32 and the result is rounded once; the order of the sums
- * depends on the sizes only.  addend may be NULL, or c itself with the same
- * pitch (to add to a gradient); dropout (NULL: none) applies to the product as
- * demo_dropout does, element i*n + j.  c and addend [m][n] with row pitches
- * ldc and ld_addend in elements, aligned to their element.  m, n at most 2^30,
- * k at most DEMO_BLOCK_MAX_K (DEMO_EUNSUPPORTED beyond).  The workspace is
- * written by the call and free again when it has run: calls that may run at
- * the same time (other streams, other graphs) need one each.
+ * depends on the sizes only.  For an fp32 result products and sums have fp32's
+ * precision for operand values between 2^-126 and 2^128; for 16-bit results
+ * the hardware lines up eight neighbouring products of the sum at the largest
+ * of them and keeps 13 binary places below it (on random data 1.4e-5 of the
+ * result, a hundredth of its rounding).  addend may be NULL, or c itself with
+ * the same pitch (to add to a gradient); dropout (NULL: none) applies to the
+ * product as demo_dropout does, element i*n + j.  c and addend [m][n] with row
+ * pitches ldc and ld_addend in elements, aligned to their element, (m - 1)*ldc
+ * and (m - 1)*ld_addend at most 2^40.  m, n at most 2^30, k at most
+ * DEMO_BLOCK_MAX_K (DEMO_EUNSUPPORTED beyond), each of m*n, m*k and n*k at most
+ * DEMO_MAX_ELEMS.  The workspace is written by the call and free again when it
+ * has run: calls that may run at the same time (other streams, other graphs)
+ * need one each.
  */
 int demo_block_matmul(const demo_product_cfg *cfg, uint64_t m, uint64_t n, uint64_t k, const void *a, const void *b,
                       void *c, uint64_t ldc, const void *addend, uint64_t ld_addend,

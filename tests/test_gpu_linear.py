@@ -435,6 +435,24 @@ def test_product_with_addend_and_dropout(torch, m, n, k, out, p):
         assert (wide[:, :at] == 3).all() and (wide[:, at + n:] == 3).all()
 
 
+@pytest.mark.parametrize("m", [1, 2, 3, 17])
+def test_product_of_millions_of_columns(torch, m):
+    """More columns than the grids of the kernels for few rows hold."""
+    n, k = (1 << 24) + 70, 128
+    x, w = normal(torch, 1, m, k), torch.zeros(n, k, dtype=torch.bfloat16, device="cuda")
+    at = [0, 77, (1 << 22) - 1, 1 << 22, (1 << 24) + 69]
+    w[at] = normal(torch, 2, len(at), k, dtype=torch.bfloat16)
+    a, b = operand(torch, m, k), operand(torch, n, k)
+    L.demo_block_quantize(L.Block(), x, a)
+    L.demo_block_quantize(L.Block(), w, b)
+    c = torch.full((m, n), 3.0, device="cuda")
+    L.demo_block_matmul(L.Product(), m, n, k, a, b, c, workspace=workspace(torch, m, n, k))
+    check_product(torch, c[:, at], F.value(*F.quantize(host(x), 0, 0)), F.value(*F.quantize(host(w[at]), 0, 0)))
+    rest = torch.ones(n, dtype=torch.bool, device="cuda")
+    rest[at] = False
+    assert not c[:, rest].any()
+
+
 def test_product_range_of_scales(torch):
     """The smallest and largest scale bytes; zero rows; NaN codes reach their row or column only."""
     m, n, k = 40, 48, 256

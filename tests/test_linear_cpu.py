@@ -97,6 +97,7 @@ def test_quantize_refusals():
     for bad in (L.Block(fmt=2).c(0), L.Block(tile=2).c(0), L.Block().c(3)):
         assert call(bad) == L.EINVAL
     assert call(rows=0) == call(cols=0) == call(ld=199) == call(src=None) == L.EINVAL
+    assert call(ld=2**36) == L.EINVAL  # (rows - 1) ld past 2^40
     assert call(rows=2**30 + 1) == call(q=None, qt=None) == L.EINVAL
     assert call(src=FAR + 1) == call(q=2 * FAR + 8) == call(qt=3 * FAR + 4) == L.EALIGN
     assert call(q=FAR + 1024) == call(qt=FAR - 1024) == call(qt=2 * FAR + 256) == L.EINVAL  # overlaps
@@ -112,6 +113,7 @@ def test_matmul_refusals():
         assert call(bad) == L.EINVAL
     assert call(m=0) == call(n=0) == call(k=0) == call(ldc=95) == L.EINVAL
     assert call(a=None) == call(b=None) == call(c=None) == L.EINVAL
+    assert call(ldc=2**36) == call(addend=4 * FAR, ld_addend=2**36) == L.EINVAL  # (m - 1) ldc past 2^40
     assert call(k=L.BLOCK_MAX_K + 1) == L.EUNSUPPORTED
     assert call(m=2**30 + 1) == L.EINVAL
     assert call(a=FAR + 8) == call(b=2 * FAR + 4) == call(c=3 * FAR + 1) == L.EALIGN
