@@ -335,8 +335,7 @@ def demo_payload_validate(cfg, n_elems: int, payload, violations_out, stream=Non
     pb = _payload_bytes(c, n_elems) if _sends(c) else 0
     _check(lib().demo_payload_validate(ctypes.byref(c), n_elems, _buf(payload, "payload", pb),
                                        _buf(violations_out, "violations_out", 8, elem=8), _stream(stream)),
-           "demo_payload_validate", "demo_dropout", "demo_dropout_backward", "demo_block_layout",
-           "demo_block_quantize", "demo_block_workspace", "demo_block_matmul")
+           "demo_payload_validate")
 
 
 def demo_encode_adamw(cfg, adamw, n_elems: int, grad, moment1, moment2, payload_out, q_out=None,
