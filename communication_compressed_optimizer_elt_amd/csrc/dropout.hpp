@@ -47,9 +47,9 @@ __device__ __forceinline__ void drop_block(const Drop& d, uint64_t blk, float (&
     drop_drawn(d, w, v);
 }
 
-// the same for elements e + j, e counted from the tensor's element 0: they
-// may reach into the next block
-__device__ __forceinline__ void drop8(const Drop& d, uint64_t e, float (&v)[8]) {
+// bit j: element e + j is kept, e counted from the tensor's element 0 (they may
+// reach into the next block)
+__device__ __forceinline__ uint32_t kept8(const Drop& d, uint64_t e) {
     const uint64_t blk = d.first + (e >> 3);
     const uint32_t from = (uint32_t)e & 7u;
     uint32_t w[4], keep = 0;
@@ -61,7 +61,12 @@ __device__ __forceinline__ void drop8(const Drop& d, uint64_t e, float (&v)[8]) 
 #pragma unroll
         for (int j = 0; j < 8; j++) keep |= (uint32_t)((w[j >> 1] >> 16 * (j & 1) & 0xFFFFu) >= d.threshold) << (8 + j);
     }
-    keep >>= from;
+    return keep >> from;
+}
+
+// v[j] = element e + j is kept ? v[j] * scale : 0
+__device__ __forceinline__ void drop8(const Drop& d, uint64_t e, float (&v)[8]) {
+    const uint32_t keep = kept8(d, e);
 #pragma unroll
     for (int j = 0; j < 8; j++) v[j] = keep >> j & 1 ? v[j] * d.scale : 0.f;
 }

@@ -4,6 +4,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <cstring>
 
 #include "demo.h"
 #include "host.hpp"
@@ -89,6 +90,21 @@ int dropout_impl(const demo_dropout_cfg* cfg, uint32_t dtype, uint64_t n, const 
     case DEMO_DTYPE_F16: return status_of(launch_dropout<demo::f16_t>(a, s));
     default: return status_of(launch_dropout<demo::bf16_t>(a, s));
     }
+}
+
+// least magnitude of a 16-bit type, as its bits, whose product with `scale` (0
+// or at least 1) is infinite or NaN in fp32
+uint32_t odd_from(uint32_t dtype, float scale) {
+    if (dtype != DEMO_DTYPE_BF16) return 0x7C00u;  // fp16 times 65536 is far below fp32's largest
+    const auto value = [](uint32_t u) {
+        u <<= 16;
+        float f;
+        std::memcpy(&f, &u, 4);
+        return f;
+    };
+    uint32_t u = 0x7F80u;
+    while (u && !std::isfinite(value(u - 1) * scale)) u--;
+    return u;
 }
 
 template <typename T, int FMT, bool TILE>
@@ -238,6 +254,7 @@ int demo_block_quantize(const demo_block_cfg* cfg, uint64_t rows, uint64_t cols,
         return DEMO_EINVAL;
     a.src = src;
     a.ld = ld;
+    a.odd_from = odd_from(cfg->dtype, a.drop.scale);
     a.rows = (uint32_t)rows;
     a.cols = (uint32_t)cols;
     if (operand) {

@@ -18,7 +18,7 @@
 // Bound by memory: 16384 x 8192 bf16 to e4m3, both operands (537 MB), takes 99
 // us (5.4 TB/s; 112 us before the pieces of a transposed row were written side
 // by side and the source read past the caches); 8192 x 2048 fp32 in squares
-// (101 MB) 24 us and 16384 x 2048 bf16 through a dropout to e5m2 (134 MB) 35 us,
+// (101 MB) 24 us and 16384 x 2048 bf16 through a dropout to e5m2 (134 MB) 36 us,
 // one or two rounds of workgroups whose loads, arithmetic and stores coincide.
 // Workgroups that stay and load their next square early spilled and took twice
 // as long (54 us for the fp32 weight).
@@ -43,6 +43,7 @@ struct QuantArgs {
     uint64_t pitch_t;
     uint32_t s_pitch_t;
     uint32_t tiles_c;     // column tiles
+    uint32_t odd_from;    // 16-bit sources: least magnitude whose product with the dropout's scale is no number
     Drop drop;
 };
 
@@ -108,28 +109,29 @@ __device__ __forceinline__ s2 codes2(s2 old, uint32_t pair, float scale) {
     }
 }
 
-// A work-item's 8 x 8 values as floats (fp32 sources, and what a dropout has
-// scaled): magnitudes are compared as fp32 bits.
+// A work-item's 8 x 8 values as floats: magnitudes are compared as fp32 bits.
+// Those from `from` on are no numbers.
 struct FloatSquare {
     static constexpr bool kPacked = false;
+    static constexpr uint32_t kInf = 0x7F800000u;
     float v[8][8];
 
-    static __device__ __forceinline__ bool odd(uint32_t u) { return u >= 0x7F800000u; }  // infinity or NaN
+    static __device__ __forceinline__ bool odd(uint32_t u, uint32_t from) { return u >= from; }
     // magnitude; FINITE: 0 for infinity and NaN
     template <bool FINITE>
-    __device__ __forceinline__ uint32_t size(int i, int j) const {
+    __device__ __forceinline__ uint32_t size(int i, int j, uint32_t from) const {
         const uint32_t u = __float_as_uint(v[i][j]) & 0x7FFFFFFFu;
-        return FINITE && odd(u) ? 0u : u;
+        return FINITE && u >= from ? 0u : u;
     }
     // maxima of the rows and of the columns, words of 32 bits
     template <bool FINITE>
-    __device__ __forceinline__ void maxima(uint32_t (&r)[8], uint32_t (&c)[8]) const {
+    __device__ __forceinline__ void maxima(uint32_t (&r)[8], uint32_t (&c)[8], uint32_t from) const {
 #pragma unroll
         for (int i = 0; i < 8; i++) {
             r[i] = 0;
 #pragma unroll
             for (int j = 0; j < 8; j++) {
-                const uint32_t u = size<FINITE>(i, j);
+                const uint32_t u = size<FINITE>(i, j, from);
                 r[i] = max(r[i], u);
                 c[j] = i ? max(c[j], u) : u;
             }
@@ -143,12 +145,12 @@ struct FloatSquare {
 #pragma unroll
             for (int j = 0; j < 8; j++) asm volatile("" : "+v"(v[i][j]));
     }
-    __device__ __forceinline__ void infinities_to_nan() {
+    __device__ __forceinline__ void odd_to_nan(uint32_t from) {
 #pragma unroll
         for (int i = 0; i < 8; i++)
 #pragma unroll
             for (int j = 0; j < 8; j++)
-                if (odd(__float_as_uint(v[i][j]) & 0x7FFFFFFFu)) v[i][j] = __uint_as_float(0x7FC00000u);
+                if ((__float_as_uint(v[i][j]) & 0x7FFFFFFFu) >= from) v[i][j] = __uint_as_float(0x7FC00000u);
     }
     template <int FMT>
     __device__ __forceinline__ uint2_v row_codes(int i, float k) const {
@@ -174,23 +176,25 @@ struct PairSquare {
     static constexpr uint32_t kInf = __is_same(T, bf16_t) ? 0x7F80u : 0x7C00u;
     uint32_t v[8][4];
 
-    static __device__ __forceinline__ bool odd(uint32_t u) { return (u & 0x7FFFu) >= kInf || (u >> 16 & 0x7FFFu) >= kInf; }
+    static __device__ __forceinline__ bool odd(uint32_t u, uint32_t from) {
+        return (u & 0x7FFFu) >= from || (u >> 16 & 0x7FFFu) >= from;
+    }
     template <bool FINITE>
-    __device__ __forceinline__ uint32_t size(int i, int j) const {
+    __device__ __forceinline__ uint32_t size(int i, int j, uint32_t from) const {
         uint32_t u = v[i][j] & 0x7FFF7FFFu;
-        if (FINITE && (u & 0xFFFFu) >= kInf) u &= 0xFFFF0000u;
-        if (FINITE && (u >> 16) >= kInf) u &= 0xFFFFu;
+        if (FINITE && (u & 0xFFFFu) >= from) u &= 0xFFFF0000u;
+        if (FINITE && (u >> 16) >= from) u &= 0xFFFFu;
         return u;
     }
     // maxima of the rows, and of the columns as pairs
     template <bool FINITE>
-    __device__ __forceinline__ void maxima(uint32_t (&r)[8], uint32_t (&c)[4]) const {
+    __device__ __forceinline__ void maxima(uint32_t (&r)[8], uint32_t (&c)[4], uint32_t from) const {
 #pragma unroll
         for (int i = 0; i < 8; i++) {
             uint32_t row = 0;
 #pragma unroll
             for (int j = 0; j < 4; j++) {
-                const uint32_t u = size<FINITE>(i, j);
+                const uint32_t u = size<FINITE>(i, j, from);
                 row = j ? pk_max(row, u) : u;
                 c[j] = i ? pk_max(c[j], u) : u;
             }
@@ -204,14 +208,43 @@ struct PairSquare {
 #pragma unroll
             for (int j = 0; j < 4; j++) asm volatile("" : "+v"(v[i][j]));
     }
-    __device__ __forceinline__ void infinities_to_nan() {
+    __device__ __forceinline__ void odd_to_nan(uint32_t from) {
 #pragma unroll
         for (int i = 0; i < 8; i++)
 #pragma unroll
             for (int j = 0; j < 4; j++) {
-                if ((v[i][j] & 0x7FFFu) >= kInf) v[i][j] |= 0x7FFFu;
-                if ((v[i][j] >> 16 & 0x7FFFu) >= kInf) v[i][j] |= 0x7FFF0000u;
+                if ((v[i][j] & 0x7FFFu) >= from) v[i][j] |= 0x7FFFu;
+                if ((v[i][j] >> 16 & 0x7FFFu) >= from) v[i][j] |= 0x7FFF0000u;
             }
+    }
+    // draws become masks of what a dropout leaves out (a threshold below 65536)
+    static __device__ __forceinline__ void left_out(uint32_t (&w)[4], uint32_t threshold) {
+        const us2 t = {(uint16_t)threshold, (uint16_t)threshold};
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            us2 out = __builtin_elementwise_sub_sat(t, __builtin_bit_cast(us2, w[j]));  // 0: kept
+            out = __builtin_elementwise_min(out, us2{1, 1}) * us2{0xFFFF, 0xFFFF};
+            w[j] = __builtin_bit_cast(uint32_t, out);
+        }
+    }
+    // row i without that, or with a bit for each value it keeps
+    __device__ __forceinline__ void drop_out(int i, const uint32_t (&w)[4]) {
+#pragma unroll
+        for (int j = 0; j < 4; j++) v[i][j] &= ~w[j];
+    }
+    __device__ __forceinline__ void drop_kept(int i, uint32_t keep) {
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+            v[i][j] &= (keep >> 2 * j & 1 ? 0xFFFFu : 0u) | (keep >> (2 * j + 1) & 1 ? 0xFFFF0000u : 0u);
+    }
+    // the values times a scale
+    __device__ __forceinline__ FloatSquare times(float scale) const {
+        FloatSquare f;
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+#pragma unroll
+            for (int j = 0; j < 8; j++) f.v[i][j] = number(v[i][j >> 1] >> 16 * (j & 1)) * scale;
+        return f;
     }
     template <int FMT>
     __device__ __forceinline__ uint2_v row_codes(int i, float k) const {
@@ -265,19 +298,14 @@ __device__ __forceinline__ void load_each(const float* src, uint32_t left, float
         if ((uint32_t)j < left) v[j] = src[j];
 }
 
-// fp32 bits of a maximum as the square keeps it
-template <typename SQ, typename T>
-__device__ __forceinline__ uint32_t float_bits(uint32_t u) {
-    if constexpr (SQ::kPacked) return __float_as_uint(SQ::number(u));
-    else return u;
-}
-
-// DROP: the source through a dropout's gradient, as floats.  WIDE: rows of src
-// are 16-byte aligned and cols a multiple of 8.
+// DROP: the source through a dropout's gradient.  A product with the scale, in
+// fp32, grows with the value: 16-bit sources find their maxima, and what
+// overflows, as pairs without the scale (16384 x 2048 bf16 36 us, as products
+// 37.5 us; 8192 x 2048 20 and 22 us).  WIDE: rows of src are 16-byte aligned and cols a multiple of 8.
 template <typename T, int FMT, bool TILE, bool DROP, bool WIDE>
 __global__ __launch_bounds__(256, 4) void quantize_kernel(QuantArgs p) {
-    typedef typename std::conditional<DROP, FloatSquare, Square<T>>::type SQ;
-    constexpr int kCols = SQ::kPacked ? 4 : 8;  // words of a work-item's columns' maxima
+    typedef Square<T> SQ;
+    constexpr int kCols = SQ::kPacked ? 4 : 8;  // words of a work-item's columns' maxima, and of a row
     __shared__ __attribute__((aligned(16))) uint32_t colmax[4][16 * kCols];
     __shared__ __attribute__((aligned(16))) uint8_t turned[kBlk * kBlk];
     const int t = threadIdx.x, g = t >> 4, h = t & 15, wave = t >> 6;
@@ -289,69 +317,80 @@ __global__ __launch_bounds__(256, 4) void quantize_kernel(QuantArgs p) {
 
     SQ sq;
     {
-        constexpr int kWords = Square<T>::kPacked ? 4 : 8;
         const T* src = (const T*)p.src;
-        Square<T> raw;
         if (WIDE) {
             // what lies outside repeats the last row or columns, and becomes zero
             const uint32_t c = min(c0, p.cols - 8);
 #pragma unroll
-            for (int i = 0; i < 8; i++) load_wide(src + (uint64_t)min(r0 + i, p.rows - 1) * p.ld + c, raw.v[i]);
+            for (int i = 0; i < 8; i++) load_wide(src + (uint64_t)min(r0 + i, p.rows - 1) * p.ld + c, sq.v[i]);
         } else {
 #pragma unroll
             for (int i = 0; i < 8; i++) {
 #pragma unroll
-                for (int j = 0; j < kWords; j++) raw.v[i][j] = 0;
-                if (r0 + i < p.rows && c0 < p.cols) load_each(src + (uint64_t)(r0 + i) * p.ld + c0, p.cols - c0, raw.v[i]);
+                for (int j = 0; j < kCols; j++) sq.v[i][j] = 0;
+                if (r0 + i < p.rows && c0 < p.cols) load_each(src + (uint64_t)(r0 + i) * p.ld + c0, p.cols - c0, sq.v[i]);
             }
         }
         uint32_t drawn[8][4];
         if (WIDE && DROP) {  // drawn while the loads are under way
 #pragma unroll
-            for (int i = 0; i < 8; i++)
+            for (int i = 0; i < 8; i++) {
                 draw_block(p.drop, p.drop.first + (((uint64_t)(r0 + i) * p.cols + c0) >> 3), drawn[i]);
+                if constexpr (SQ::kPacked) SQ::left_out(drawn[i], p.drop.threshold);
+            }
             __builtin_amdgcn_sched_barrier(0);
         }
-        if (WIDE && ((tr + 1) * kBlk > p.rows || (tc + 1) * kBlk > p.cols)) {
+        const bool past = WIDE && ((tr + 1) * kBlk > p.rows || (tc + 1) * kBlk > p.cols);
+        const bool none = DROP && SQ::kPacked && p.drop.threshold == 65536u;  // nothing is kept
+        if (past || none) {
 #pragma unroll
             for (int i = 0; i < 8; i++)
 #pragma unroll
-                for (int j = 0; j < kWords; j++)
-                    if (r0 + i >= p.rows || c0 >= p.cols) raw.v[i][j] = 0;
+                for (int j = 0; j < kCols; j++)
+                    if (none || r0 + i >= p.rows || c0 >= p.cols) sq.v[i][j] = 0;
         }
-        if constexpr (!DROP) {
-            static_cast<Square<T>&>(sq) = raw;
-        } else {
+        if constexpr (DROP) {
 #pragma unroll
             for (int i = 0; i < 8; i++) {
-#pragma unroll
-                for (int j = 0; j < 8; j++) {
-                    if constexpr (Square<T>::kPacked) sq.v[i][j] = Square<T>::number(raw.v[i][j >> 1] >> 16 * (j & 1));
-                    else sq.v[i][j] = raw.v[i][j];
+                const uint64_t e = (uint64_t)(r0 + i) * p.cols + c0;
+                if constexpr (SQ::kPacked) {
+                    if (WIDE) sq.drop_out(i, drawn[i]);
+                    else sq.drop_kept(i, kept8(p.drop, e));
+                } else {
+                    if (WIDE) drop_drawn(p.drop, drawn[i], sq.v[i]);
+                    else drop8(p.drop, e, sq.v[i]);
                 }
-                if (WIDE) drop_drawn(p.drop, drawn[i], sq.v[i]);
-                else drop8(p.drop, (uint64_t)(r0 + i) * p.cols + c0, sq.v[i]);
             }
         }
     }
+    const uint32_t odd_from = DROP && SQ::kPacked ? p.odd_from : SQ::kInf;
+    // fp32 bits of a maximum as the square keeps it
+    auto float_bits = [&](uint32_t u) {
+        if constexpr (SQ::kPacked) return __float_as_uint(DROP ? SQ::number(u) * p.drop.scale : SQ::number(u));
+        else return u;
+    };
     uint32_t rowmax[8], cmax[kCols], any = 0;
-    sq.template maxima<false>(rowmax, cmax);
+    sq.template maxima<false>(rowmax, cmax, odd_from);
 #pragma unroll
-    for (int j = 0; j < kCols; j++) any |= SQ::odd(cmax[j]);
+    for (int j = 0; j < kCols; j++) any |= SQ::odd(cmax[j], odd_from);
     if (any) {  // infinities and NaN: no part of a maximum, and NaN in the end
         sq.renew();
-        sq.template maxima<true>(rowmax, cmax);
-        sq.infinities_to_nan();
+        sq.template maxima<true>(rowmax, cmax, odd_from);
+        sq.odd_to_nan(odd_from);
     }
+    const auto out = [&] {
+        if constexpr (DROP && SQ::kPacked) return sq.times(p.drop.scale);
+        else return sq;
+    }();
 #pragma unroll
     for (int i = 0; i < 8; i++) rowmax[i] = max16(rowmax[i]);
     auto rows_out = [&] {
         if (p.q) {
 #pragma unroll
             for (int i = 0; i < 8; i++) {
-                const uint32_t r = r0 + i, b = scale_byte<FMT>(float_bits<SQ, T>(rowmax[i]));
+                const uint32_t r = r0 + i, b = scale_byte<FMT>(float_bits(rowmax[i]));
                 if (r < p.rows) {
-                    *(uint2_v*)(p.q + (uint64_t)r * p.pitch + c0) = sq.template row_codes<FMT>(i, scale_of(b));
+                    *(uint2_v*)(p.q + (uint64_t)r * p.pitch + c0) = out.template row_codes<FMT>(i, scale_of(b));
                     if (h == 0) {
                         uint8_t* s = p.s + (uint64_t)r * p.s_pitch;
                         s[tc] = (uint8_t)b;
@@ -397,8 +436,8 @@ __global__ __launch_bounds__(256, 4) void quantize_kernel(QuantArgs p) {
 #pragma unroll
         for (int j = 0; j < 8; j++) {
             const int c = h * 8 + j;
-            const uint32_t b = scale_byte<FMT>(float_bits<SQ, T>(colbits[j]));
-            *(uint2_v*)(turned + c * kBlk + 8 * (g ^ h)) = sq.template col_codes<FMT>(j, scale_of(b));
+            const uint32_t b = scale_byte<FMT>(float_bits(colbits[j]));
+            *(uint2_v*)(turned + c * kBlk + 8 * (g ^ h)) = out.template col_codes<FMT>(j, scale_of(b));
             if (g == 0 && c0 + j < p.cols) {
                 uint8_t* s = p.st + (uint64_t)(c0 + j) * p.s_pitch_t;
                 s[tr] = (uint8_t)b;

@@ -277,6 +277,33 @@ def test_quantize_with_dropout(torch, rows, cols, dtype):
     check_operand(torch, qt, g.T, 1, 0)
 
 
+@pytest.mark.parametrize("p", [0.0, 0.1, 0.5, 1.0 - 2.0**-16, 1.0])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("cols", [200, 203])
+def test_quantize_with_dropout_at_the_range_end(torch, cols, dtype, p):
+    """Kept values whose product with the scale overflows fp32 are infinite:
+    NaN codes, and no part of a block's largest magnitude.  What is dropped
+    leaves nothing, NaN and infinities included."""
+    rows = 140
+    x = normal(torch, 14, rows, cols, dtype=dt(torch, dtype))
+    top = torch.finfo(x.dtype).max
+    x[1::9, ::5] = top
+    x[2::9, ::7] = -top * 0.93
+    x[3::9, 1::4] = top / 1.99
+    x[4::9, 2::11] = float("inf")
+    x[5::9, 3::6] = float("nan")
+    x[6::9] *= torch.finfo(x.dtype).tiny
+    kw = dict(p=p, seed=5, step=1, site=3)
+    for tile in (0, 1):
+        q, qt = operand(torch, rows, cols), operand(torch, cols, rows)
+        L.demo_block_quantize(L.Block(fmt=1, tile=tile), x, q, qt, dropout=L.Dropout(**kw))
+        with np.errstate(over="ignore", invalid="ignore"):
+            g = np.float32(host(x)) * np.float32(F.scale(p))
+        g = np.where(F.keep(rows * cols, **kw).reshape(rows, cols), g, np.float32(0))
+        check_operand(torch, q, g, 1, tile)
+        check_operand(torch, qt, g.T, 1, tile)
+
+
 def test_quantize_beyond_2_pow_32_bytes(torch):
     """The last rows of a source and an operand of more than 2^32 elements."""
     rows, cols = (1 << 21) + 130, 2048
