@@ -156,8 +156,9 @@ struct Plan {
 //    against 19.9 us), so they are taken where rounds say so at 1.65;
 //  * up to 256 tiles of 128, tiles of 64 fill the card better (1024 x 2048 x
 //    2048: 9.2 against 14.6 us; 2048 x 2048 x 2048, 256 tiles: 15.8 against 16.6
-//    us, 23.6 against 29.7 us with an fp32 result); with a sum of 8192 or more
-//    up to 192 (2048 x 2048 x 8192: 54 against 53 us, 85 against 79 us);
+//    us, 24.1 against 28.7 us with an fp32 result); 16-bit results with a sum of
+//    8192 or more up to 192 (2048 x 2048 x 8192: 54 against 53 us, but 75 against
+//    85 us with an fp32 result);
 //  * the sum is split where tiles fill less than a round: down to 16 blocks of
 //    128 for tiles of 64 (256 x 2048 x 8192: 16.4 us in 4, 23.8 in one; 128 x
 //    2048 x 2048: 7.6 us in one, 9.7 in 2), to 64 for tiles of 128 (2048 x 2048
@@ -171,7 +172,7 @@ Plan plan_of(uint64_t m, uint64_t n, uint64_t k, bool wide) {
     const auto rounds = [](uint64_t count, uint64_t at_once) { return (count + at_once - 1) / at_once; };
     if (m >= 256 && n >= 256 && (wide ? 37 : 33) * rounds(tiles(256), 256) <= 20 * rounds(tiles(128), 512))
         return {256, 1, (uint32_t)up(kb, 4)};
-    const uint64_t tile = tiles(128) > (kb >= 64 ? 192u : 256u) ? 128 : 64, least = tile == 128 ? 64 : 16;
+    const uint64_t tile = tiles(128) > (kb >= 64 && !wide ? 192u : 256u) ? 128 : 64, least = tile == 128 ? 64 : 16;
     uint64_t splits = 512 / tiles(tile);
     if (splits > kb / least) splits = kb / least;
     if (splits < 1) splits = 1;
@@ -183,8 +184,9 @@ static_assert(512 * 128 * 128 * 4 <= DEMO_BLOCK_MAX_WORKSPACE, "workspace");
 
 template <int FA, int FB, bool WIDE, int TILE>
 hipError_t launch_tiles(const demo::ProductArgs& a, dim3 grid, hipStream_t s) {
-    return launch(demo::product_kernel<FA, FB, WIDE, TILE, TILE, 2, 2>, grid, dim3(256),
-                  2 * 2 * TILE * (DEMO_BLOCK + 4), s, a);
+    const size_t lds = 2 * 2 * TILE * (DEMO_BLOCK + 4);
+    if constexpr (WIDE && TILE == 64) return launch(demo::product_shared_kernel<FA, FB>, grid, dim3(256), lds, s, a);
+    else return launch(demo::product_kernel<FA, FB, WIDE, TILE, TILE, 2, 2>, grid, dim3(256), lds, s, a);
 }
 
 template <int FA, int FB, bool WIDE>

@@ -220,7 +220,7 @@ typedef __bf16 v8b __attribute__((ext_vector_type(8)));
 
 // 2^(byte - 127)
 __device__ __forceinline__ float scale_float(uint32_t byte) {
-    return __uint_as_float(byte ? byte << 23 : 0x00400000u);
+    return __uint_as_float(max(byte << 23, 0x00400000u));
 }
 
 // eight codes (two words) as bf16 times their scale: exact
@@ -307,12 +307,13 @@ __device__ __forceinline__ void sync_loads() {
 // LDS one block ahead; one barrier a block.  What hides the waits is a second
 // workgroup on the CU (four of 64 x 64): three or four stages, and with them
 // fewer workgroups, measured slower (2048 x 2048 x 2048 in tiles of 64: 15.8
-// us, 19.2 and 18.2 with three and four; 4096 x 8192 x 2048 in tiles of 128:
-// 71 us, 112 with four), and so did 8 waves of half the size (17.6 us).  Row
-// r's 16-byte chunk c sits at c ^ (r / 2 & 7), which spreads 16 rows' reads of
-// one chunk over all 64 banks; loads into LDS write lanes in order, so the
-// exchange is made on their source addresses.
-// Rows past the matrix repeat its last row; what they give is not stored.
+// us, 19.2 and 18.2 with three and four; 11.8 against 12.0 us at 2304 x 768 x
+// 2560, where no CU has more than two; 4096 x 8192 x 2048 in tiles of 128: 71
+// us, 112 with four), and so did 8 waves of half the size (17.6 us).  Row r's
+// 16-byte chunk c sits at c ^ (r / 2 & 7), which spreads 16 rows' reads of one
+// chunk over all 64 banks; loads into LDS write lanes in order, so the exchange
+// is made on their source addresses.  Fp32 results in tiles of 64 have a kernel
+// of their own below.  Rows past the matrix repeat its last row; what they give is not stored.
 template <int FA, int FB, bool WIDE, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN) void product_kernel(ProductArgs p) {
     constexpr int NW = WM * WN, SM = BM / WM / 16, SN = BN / WN / 16;
@@ -397,6 +398,115 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(ProductArgs p) {
     __syncthreads();
     finish<SM, SN>(target(p, blockIdx.y), acc, (float*)(lds + wave * finish_bytes<SM, SN>()), m0 + wm * SM * 16,
                    n0 + wn * SN * 16, 0, 0, lane);
+}
+
+// 64 x 64 of C with an fp32 result: four waves that share the sum, a quarter of
+// each block of 128 each.  A wave then widens 32 codes of 64 rows of both
+// operands for its 16 matrix instructions, half of what it would widen for 32 x
+// 32 of C and the whole block: 2304 x 768 x 2560 takes 17.2 us (18.8 so), 2048 x
+// 2048 x 8192 75 us (85 so).  Bound by issue: widening and matrix instructions
+// of a SIMD's waves take turns; two blocks a barrier gave nothing (19.4 against
+// 18.4 us with an addend).  Loads, stages and chunks as in product_kernel.  In
+// the end wave w takes rows 16 w .. +15 and adds the others' sums in the order
+// w, w+3, w+2, w+1 (mod 4): three exchanges through two halves of LDS.
+template <int FA, int FB>
+__global__ __launch_bounds__(256, 4) void product_shared_kernel(ProductArgs p) {
+    constexpr int T = 64, kStage = 2 * T * kBlkK, kScales = 2 * T * 4, kPiece = 64 * 4 * 16;
+    static_assert(8 * kPiece <= 2 * kStage && 4 * finish_bytes<1, 4>() <= 2 * kStage, "the way out fits the stages");
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    const uint8_t* scales = lds + 2 * kStage;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    uint32_t tm, tn;
+    tile_of(p.tiles_m, p.tiles_n, blockIdx.x, tm, tn);
+    const uint32_t m0 = tm * T, n0 = tn * T;
+    const uint32_t kb0 = blockIdx.y * p.kb_split, kb1 = min(kb0 + p.kb_split, p.kb);
+    const uint32_t lds0 = __builtin_amdgcn_readfirstlane(
+        (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds);
+
+    // this lane's place in the loads: row 8 (wave + 4 i) + lane / 8
+    const uint8_t* ga = p.a + (uint64_t)m0 * p.pitch;
+    const uint8_t* gb = p.b + (uint64_t)n0 * p.pitch;
+    uint32_t oa[2], ob[2];
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        const uint32_t r = 8 * (wave + i * 4) + (lane >> 3), c = ((lane & 7) ^ (r >> 1 & 7)) * 16;
+        oa[i] = min(r, p.m - 1 - m0) * p.pitch + c;
+        ob[i] = min(r, p.n - 1 - n0) * p.pitch + c;
+    }
+    const uint32_t srow = min((uint32_t)lane, wave ? p.n - 1 - n0 : p.m - 1 - m0);
+    const uint8_t* gs = wave ? p.sb + (uint64_t)n0 * p.s_pitch : p.sa + (uint64_t)m0 * p.s_pitch;
+    const uint32_t os = srow * p.s_pitch;
+    auto fetch = [&](uint32_t kb) {
+        const uint32_t at = lds0 + (kb & 1) * kStage;
+#pragma unroll
+        for (int i = 0; i < 2; i++) load_lds16(ga + kb * kBlkK, oa[i], at + (wave + i * 4) * 1024);
+#pragma unroll
+        for (int i = 0; i < 2; i++) load_lds16(gb + kb * kBlkK, ob[i], at + T * kBlkK + (wave + i * 4) * 1024);
+        if ((kb & 3) == 0 && wave < 2)  // four blocks' scale bytes
+            load_lds4(gs + kb, os, lds0 + 2 * kStage + (kb >> 2 & 1) * kScales + wave * 256);
+    };
+
+    // eight codes of row `row` of a fragment: half g % 2 of chunk 2 wave + g / 2
+    const int row = lane & 15, g = lane >> 4;
+    const uint32_t at = row * kBlkK + ((2 * wave + (g >> 1)) ^ (row >> 1)) * 16 + (g & 1) * 8;
+    v4f acc[4][4] = {};
+    uint32_t ea[4], eb[4];
+    fetch(kb0);
+    for (uint32_t kb = kb0; kb < kb1; kb++) {
+        // block kb has landed, and everyone has read the stage that is filled next
+        sync_loads<0>();
+        if (kb + 1 < kb1) fetch(kb + 1);
+        const uint8_t* stage = lds + (kb & 1) * kStage + at;
+        if ((kb & 3) == 0) {
+            const uint32_t* sc = (const uint32_t*)(scales + (kb >> 2 & 1) * kScales) + row;
+#pragma unroll
+            for (int i = 0; i < 4; i++) ea[i] = sc[i * 16], eb[i] = sc[T + i * 16];
+        }
+        uint2_v fa[4], fb[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) fb[i] = *(const uint2_v*)(stage + (T + i * 16) * kBlkK);
+#pragma unroll
+        for (int i = 0; i < 4; i++) fa[i] = *(const uint2_v*)(stage + i * 16 * kBlkK);
+        v8b wb[4];
+#pragma unroll
+        for (int j = 0; j < 4; j++) wb[j] = widen<FB>((int)fb[j][0], (int)fb[j][1], scale_float(eb[j] & 255u));
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const v8b wa = widen<FA>((int)fa[i][0], (int)fa[i][1], scale_float(ea[i] & 255u));
+#pragma unroll
+            for (int j = 0; j < 4; j++) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j], wa, acc[i][j], 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; i++) ea[i] >>= 8, eb[i] >>= 8;
+    }
+    __syncthreads();
+
+    v4f* half = (v4f*)lds;  // place [exchange % 2][taker][column][lane]
+    auto give = [&](int x) {  // to wave w + x
+        const int to = (wave + x) & 3;
+        pick<4>(to, [&](auto I) {
+#pragma unroll
+            for (int j = 0; j < 4; j++) half[((x & 1) * 4 + to) * 256 + j * 64 + lane] = acc[decltype(I)::value][j];
+        });
+    };
+    v4f own[1][4];
+    pick<4>(wave, [&](auto I) {
+#pragma unroll
+        for (int j = 0; j < 4; j++) own[0][j] = acc[decltype(I)::value][j];
+    });
+    auto take = [&](int x) {
+#pragma unroll
+        for (int j = 0; j < 4; j++) own[0][j] += half[((x & 1) * 4 + wave) * 256 + j * 64 + lane];
+    };
+    give(1);
+    __syncthreads();
+    give(2), take(1);
+    __syncthreads();
+    give(3), take(2);
+    __syncthreads();
+    take(3);
+    __syncthreads();
+    finish<1, 4>(target(p, blockIdx.y), own, (float*)(lds + wave * finish_bytes<1, 4>()), m0 + wave * 16, n0, 0, 0, lane);
 }
 
 // 32 codes from a 16-byte aligned address
