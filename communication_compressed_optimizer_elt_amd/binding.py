@@ -262,23 +262,31 @@ def _sends(c) -> bool:
     return c.scheme != SCHEME_DILOCO or (c.period >= 1 and c.step % c.period == c.period - 1)
 
 
-_current = None  # () -> the current stream's handle
+_current = None  # device -> the handle of its current stream
+_device = None  # () -> the current device
 
 
-def _stream(stream) -> int | None:
+def _look_up() -> None:
+    """The calls behind torch's own: making a Stream object takes 2.7 us."""
+    global _current, _device
+    import torch
+
+    _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    _current = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
+                or (lambda device: torch.cuda.current_stream(device).cuda_stream))
+
+
+def _stream(stream, device: int | None = None) -> int | None:
+    """Handle of a stream; None: the current one of `device`, or of the current device."""
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
-    global _current
     if _current is None:
+        _look_up()
+    if device is None:
         import torch
 
-        # the handle itself where torch gives it: making a Stream object takes 2.7 us
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        if raw is None:
-            _current = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
-        else:
-            _current = lambda: raw(torch.cuda.current_device())  # noqa: E731
-    return _current()
+        device = torch.cuda.current_device()
+    return _current(device)
 
 
 def _cfg(cfg) -> demo_cfg:
@@ -381,9 +389,9 @@ def _here(t, what: str) -> int:
     """The current device, whose stream the call is queued on: t is on it."""
     if not t.is_cuda:
         raise ValueError(f"{what}: expected a device tensor")
-    import torch
-
-    dev = torch.cuda.current_device()
+    if _device is None:
+        _look_up()
+    dev = _device()
     if t.get_device() != dev:
         raise ValueError(f"{what}: on device {t.get_device()}, not the current one")
     return dev
@@ -443,14 +451,14 @@ def demo_dropout(cfg, x, y, residual=None, stream=None) -> None:
     dtype, dev = _dtype(x, "x"), _here(x, "x")
     _check(lib().demo_dropout(_ref(cfg), dtype, x.numel(), _flat(x, "x", x, dev),
                               None if residual is None else _flat(residual, "residual", x, dev),
-                              _flat(y, "y", x, dev), _stream(stream)), "demo_dropout")
+                              _flat(y, "y", x, dev), _stream(stream, dev)), "demo_dropout")
 
 
 def demo_dropout_backward(cfg, dy, dx, stream=None) -> None:
     """dx = the gradient of demo_dropout for x under the same cfg."""
     dtype, dev = _dtype(dy, "dy"), _here(dy, "dy")
     _check(lib().demo_dropout_backward(_ref(cfg), dtype, dy.numel(), _flat(dy, "dy", dy, dev),
-                                       _flat(dx, "dx", dy, dev), _stream(stream)), "demo_dropout_backward")
+                                       _flat(dx, "dx", dy, dev), _stream(stream, dev)), "demo_dropout_backward")
 
 
 def demo_block_layout(rows: int, cols: int) -> dict:
@@ -469,7 +477,7 @@ def demo_block_quantize(cfg, src, operand=None, operand_t=None, dropout=None, st
     c = cfg.c(_dtype(src, "src")) if isinstance(cfg, Block) else cfg
     _check(lib().demo_block_quantize(ctypes.byref(c), rows, cols, addr, ld, _ref(dropout),
                                      _operand_buf(operand, "operand", rows, cols, dev),
-                                     _operand_buf(operand_t, "operand_t", cols, rows, dev), _stream(stream)),
+                                     _operand_buf(operand_t, "operand_t", cols, rows, dev), _stream(stream, dev)),
            "demo_block_quantize")
 
 
@@ -496,7 +504,7 @@ def demo_block_matmul(cfg, m: int, n: int, k: int, a, b, c, addend=None, dropout
         work, have = _buf(workspace, "workspace", 0), workspace.numel() * workspace.element_size()
     _check(lib().demo_block_matmul(ctypes.byref(cc), m, n, k, _operand_buf(a, "a", m, k, dev),
                                    _operand_buf(b, "b", n, k, dev), addr, ldc, add, lda, _ref(dropout), work, have,
-                                   _stream(stream)), "demo_block_matmul")
+                                   _stream(stream, dev)), "demo_block_matmul")
 
 
 # raw return codes (tests of the boundary's validation)
