@@ -301,7 +301,8 @@ __device__ __forceinline__ void load_each(const float* src, uint32_t left, float
 // DROP: the source through a dropout's gradient.  A product with the scale, in
 // fp32, grows with the value: 16-bit sources find their maxima, and what
 // overflows, as pairs without the scale (16384 x 2048 bf16 36 us, as products
-// 37.5 us; 8192 x 2048 20 and 22 us).  WIDE: rows of src are 16-byte aligned and cols a multiple of 8.
+// 37.5 us; 8192 x 2048 20 and 22 us).  WIDE: rows of src are 16-byte aligned
+// and cols a multiple of 8.
 template <typename T, int FMT, bool TILE, bool DROP, bool WIDE>
 __global__ __launch_bounds__(256, 4) void quantize_kernel(QuantArgs p) {
     typedef Square<T> SQ;
