@@ -345,8 +345,11 @@ int demo_block_workspace(const demo_product_cfg *cfg, uint64_t m, uint64_t n, ui
  * depends on the sizes only.  For an fp32 result products and sums have fp32's
  * precision for operand values between 2^-126 and 2^128; for 16-bit results
  * the hardware lines up eight neighbouring products of the sum at the largest
- * of them and keeps 13 binary places below it (on random data 1.4e-5 of the
- * result, a hundredth of its rounding).  addend may be NULL, or c itself with
+ * of them and keeps 13 binary places below it.  Root mean square, relative to
+ * the result's, that is 1.5e-5 on normal values and up to 4.7e-5 where a few
+ * channels are 20 times larger: at most 1/35 of the rounding to bf16, but 1/14
+ * to 1/4 of the rounding to fp16.  An fp32 result is the way to have it exact.
+ * addend may be NULL, or c itself with
  * the same pitch (to add to a gradient); dropout (NULL: none) applies to the
  * product as demo_dropout does, element i*n + j.  c and addend [m][n] with row
  * pitches ldc and ld_addend in elements, aligned to their element, (m - 1)*ldc

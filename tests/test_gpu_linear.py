@@ -757,3 +757,95 @@ def test_binding_checks(torch):
         L.demo_dropout(L.Dropout(p=2.0), x, x)
     with pytest.raises(L.DemoError):
         L.demo_dropout(d, x[:0], x[:0])
+
+
+# ------------------------------------------------- precision of the products --
+
+def planted(m, n, k, big, small_a, small_b):
+    """One group of eight neighbours in each block of 128: big * big, -big * big
+    and a product of +-1 to +-4 times small_a small_b.  Every other product is
+    zero, so the result is the sum of the last ones, to the bit."""
+    rng = np.random.default_rng(m + n + k)
+    va, vb = np.zeros((m, k)), np.zeros((n, k))
+    for b in range(k // 128):
+        at = 128 * b + 8 * (b % 16)
+        order = rng.permutation(8)[:3]
+        va[:, at + order[0]], vb[:, at + order[0]] = big, big
+        va[:, at + order[1]], vb[:, at + order[1]] = big, -big
+        va[:, at + order[2]] = rng.choice([-2, -1, 1, 2], m) * small_a
+        vb[:, at + order[2]] = rng.choice([-2, -1, 1, 2], n) * small_b
+    return va, vb
+
+
+PLANTED = [(1, 300, 640), (2, 300, 640), (5, 200, 1280), (16, 77, 1280), (16, 4100, 128),  # one and two rows, few rows
+           (70, 130, 640), (512, 500, 8192), (33, 64, 1 << 16),                          # tiles of 64, split too
+           (1000, 5000, 256), (1800, 1900, 16512),                                        # of 128, split too
+           (2000, 8000, 384), (2040, 8184, 1152)]                                          # of 256
+
+
+@pytest.mark.parametrize("out", ["bf16", "f16"])
+@pytest.mark.parametrize("m,n,k", [s for s in PLANTED if s[2] <= 8192])
+def test_product_in_16_bits_keeps_13_places(torch, m, n, k, out):
+    """1 - 1 + 2^-13 s: the results are at most 4 k / 128 of 2^-13, which both types hold."""
+    assert 4 * k // 128 <= 256
+    va, vb = planted(m, n, k, 1.0, 2.0**-6, 2.0**-7)
+    a, b = (torch.from_numpy(F.pack(v, np.zeros((len(v), -(-k // 128)), np.int64), 0)).cuda() for v in (va, vb))
+    c = torch.full((m, n), float("nan"), dtype=dt(torch, out), device="cuda")
+    L.demo_block_matmul(L.Product(), m, n, k, a, b, c, workspace=workspace(torch, m, n, k))
+    want = torch.from_numpy(va).cuda() @ torch.from_numpy(vb).cuda().t().contiguous()
+    assert (want != 0).any() and torch.equal(c.double(), want)
+
+
+@pytest.mark.parametrize("outliers", [False, True])
+@pytest.mark.parametrize("m,n,k", [(16, 64, 2048), (48, 64, 2048), (48, 64, 8192)])
+def test_product_in_16_bits_error_of_its_sums(torch, m, n, k, outliers):
+    """What the 8-bit instructions leave of a sum.  The addend takes the rounded
+    result away, so the call returns what is below that rounding.
+    Each product loses what it has below 2^-13 of 2^(the largest sum of two
+    codes' exponents in its group of 8): the loss of a sum is at most the sum of
+    these remainders, and with their random signs the root of the sum of their
+    squares (1.5 times it, over 1024 results and more, is 30 standard deviations).
+    On such data that is less than 2^-14 of the results' root mean square."""
+    g = torch.Generator().manual_seed(k + m)
+    x, w = torch.randn(m, k, generator=g), torch.randn(n, k, generator=g) * 0.02
+    if outliers:
+        x *= torch.where(torch.rand(k, generator=g) < 0.004, 20.0, 1.0)
+    ops, values, parts = [], [], []
+    for v, tile in ((x, 0), (w, 1)):
+        codes, e = F.quantize(v.numpy(), 0, tile)
+        ops.append(torch.from_numpy(F.pack(codes, e, 0)).cuda())
+        values.append(torch.from_numpy(F.value(codes, e)).cuda())
+        low = np.maximum(np.frexp(codes)[1] - 1, -6)  # exponents of the codes
+        power = np.repeat(e, 128, 1)[:, :k] + low
+        parts.append(torch.from_numpy(np.where(codes == 0, -10**6, power)).cuda().double().view(len(v), k // 8, 8))
+    want = values[0] @ values[1].t().contiguous()
+    total = values[0].abs() @ values[1].abs().t().contiguous()
+    worst, square = torch.zeros_like(want), torch.zeros_like(want)
+    va, vb = values[0].view(m, k // 8, 8), values[1].view(n, k // 8, 8)
+    for i in range(m):
+        p = (va[i] * vb).abs()
+        q = torch.exp2((parts[0][i] + parts[1]).amax(2, keepdim=True).clamp(min=-500) - 13)
+        rest = p - torch.floor(p / q) * q
+        worst[i], square[i] = rest.sum((1, 2)), (rest * rest).sum((1, 2))
+    near = want.to(torch.float16)
+    c = torch.empty(m, n, dtype=torch.float16, device="cuda")
+    L.demo_block_matmul(L.Product(), m, n, k, *ops, c, addend=-near, workspace=workspace(torch, m, n, k))
+    err = c.double() - (want - near.double())
+    sums = (17 * (k // 128) + 64) * 2.0**-23 * total + 2.0**-23 * want.abs()
+    last = 2.0**-11 * (want - near.double()).abs() * 1.1 + 2.0**-25
+    assert (err.abs() <= worst + sums + last * 1.1).all()
+    rms = lambda t: float(t.pow(2).mean().sqrt())  # noqa: E731
+    assert rms(err) <= 1.5 * float(square.mean().sqrt()) + rms(sums) * 0.05 + rms(last)
+    assert rms(err) <= 2.0**-14 * rms(want)
+    print(f"rms of the sums' error {rms(err) / rms(want):.2e} of the result, modelled {float(square.mean().sqrt()) / rms(want):.2e}")
+
+
+@pytest.mark.parametrize("out", ["bf16", "f16"])
+def test_product_in_16_bits_is_the_same_every_time(torch, out):
+    for m, n, k in ((1, 512, 4096), (9, 512, 4096), (512, 512, 8192), (300, 200, 1000), (2048, 2048, 1024), (2500, 1100, 256), (2000, 8000, 300)):
+        a, _, b, _ = operands(torch, m, n, k)
+        ws = workspace(torch, m, n, k)
+        c = [torch.empty(m, n, dtype=dt(torch, out), device="cuda") for _ in range(3)]
+        for x in c:
+            L.demo_block_matmul(L.Product(), m, n, k, a, b, x, workspace=ws)
+        assert torch.equal(c[0], c[1]) and torch.equal(c[0], c[2])
