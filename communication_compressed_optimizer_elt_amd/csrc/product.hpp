@@ -54,15 +54,15 @@ struct ProductArgs {
 };
 
 // 64 lanes' 16 bytes at base + offset into LDS at `lds` + 16 lane, in flight
-// until the next vmcnt wait
+// until the next vmcnt wait.  The register that holds the LDS address is an
+// input, written by the compiler, which knows what is in it; one instruction
+// has to stand between that and the load.
 __device__ __forceinline__ void load_lds16(const uint8_t* base, uint32_t offset, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(offset), "s"(base)
-                 : "memory", "m0");
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"{m0}"(lds), "v"(offset), "s"(base) : "memory");
 }
 // the same with 4 bytes a lane
 __device__ __forceinline__ void load_lds4(const uint8_t* base, uint32_t offset, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(lds), "v"(offset), "s"(base)
-                 : "memory", "m0");
+    asm volatile("s_nop 0\n\tglobal_load_lds_dword %1, %2" ::"{m0}"(lds), "v"(offset), "s"(base) : "memory");
 }
 
 // C[i, j+from..j+7] from eight sums: drop, add, round once, store, element by

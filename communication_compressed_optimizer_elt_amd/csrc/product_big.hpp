@@ -19,14 +19,6 @@ constexpr size_t kBigLds = 2 * (kBigStage + kBigScales);
 
 __device__ __forceinline__ void fence_order() { __builtin_amdgcn_sched_barrier(0); }
 
-// load_lds16 to lds + IMM
-template <int IMM>
-__device__ __forceinline__ void load_at(const uint8_t* base, uint32_t offset, uint32_t lds) {
-    asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(offset), "s"(base),
-                 "n"(IMM)
-                 : "memory", "m0", "scc");
-}
-
 // d += a b, 128 along the sum, at byte Q of the scale words
 template <int FMT_A, int FMT_B, int Q>
 __device__ __forceinline__ void mma8(v4f& d, const v8i& a, const v8i& b, uint32_t ea, uint32_t eb) {
@@ -128,12 +120,12 @@ __global__ __launch_bounds__(256, 1) void product_big_kernel(ProductArgs p) {
     const uint32_t kb1 = p.kb;
     auto load_first = [&](uint32_t kb, auto ST, auto E) {  // one of 12
         constexpr int e = decltype(E)::value, x = e < 8 ? e : e < 10 ? e - 8 : e - 6;
-        load_at<decltype(ST)::value * kBigStage + (e < 8 ? kBig * kBlkK : 0) + x * 4096>(
-            (e < 8 ? t.gb : t.ga) + kb * kBlkK, t.offset + x * t.p32, t.lds);
+        load_lds16((e < 8 ? t.gb : t.ga) + kb * kBlkK, t.offset + x * t.p32,
+                   t.lds + decltype(ST)::value * kBigStage + (e < 8 ? kBig * kBlkK : 0) + x * 4096);
     };
     auto load_second = [&](uint32_t kb, auto ST, auto E) {  // one of 4
         constexpr int e = decltype(E)::value, x = e < 2 ? e + 2 : e + 4;
-        load_at<decltype(ST)::value * kBigStage + x * 4096>(t.ga + kb * kBlkK, t.offset + x * t.p32, t.lds);
+        load_lds16(t.ga + kb * kBlkK, t.offset + x * t.p32, t.lds + decltype(ST)::value * kBigStage + x * 4096);
     };
     auto load_block = [&](uint32_t kb, auto ST, auto S) {
         load_first(kb, ST, Int<0>()); load_first(kb, ST, Int<1>()); load_first(kb, ST, Int<2>());
@@ -281,8 +273,8 @@ __global__ __launch_bounds__(512, 2) void product_big_wide_kernel(ProductArgs p)
     // load x of 8 of block kb, the first 4 of A
     auto load_one = [&](uint32_t kb, auto X) {
         constexpr int x = decltype(X)::value & 3, b = decltype(X)::value >> 2;
-        load_at<b * kBig * kBlkK + x * 8192>((b ? gb : ga) + kb * kBlkK, offset + x * p64,
-                                             lds0 + wave * 1024 + (kb & 1) * kBigStage);
+        load_lds16((b ? gb : ga) + kb * kBlkK, offset + x * p64,
+                   lds0 + wave * 1024 + (kb & 1) * kBigStage + b * kBig * kBlkK + x * 8192);
     };
     auto load_bytes = [&](uint32_t kb) {
         load_lds4(gs + kb, s_offset,
