@@ -176,9 +176,11 @@ __global__ __launch_bounds__(256, 1) void product_big_kernel(ProductArgs p) {
                     if (i == 0 && two) load_first(kb + 2, Int<cur>(), Int<2 * (j - 2)>());
                     if (i == 2 && two) load_first(kb + 2, Int<cur>(), Int<2 * (j - 2) + 1>());
                     if (i == 3 && j == 7 && ((q + 2) & 3) == 0 && two) load_scales(t, kb + 2);
-                    if (i == 1 && j < 6) {
-                        fa[2 + j] = fragment(la, cur, 2 + j);
-                        if (q == 0) ea[2 + j] = sa[now + (2 + j) * 16];
+                    if constexpr (j < 6) {
+                        if (i == 1) {
+                            fa[2 + j] = fragment(la, cur, 2 + j);
+                            if (q == 0) ea[2 + j] = sa[now + (2 + j) * 16];
+                        }
                     }
                 }
                 fence_order();

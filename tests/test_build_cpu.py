@@ -45,3 +45,7 @@ def warnings(tmp_path_factory):
 
 def test_no_reserved_register_is_clobbered(warnings):
     assert not [w for w in warnings if "reserved register" in w][:3]
+
+
+def test_no_access_past_an_array(warnings):
+    assert not [w for w in warnings if "array index" in w][:3]
