@@ -521,8 +521,10 @@ __device__ __forceinline__ v8i load_codes(const uint8_t* p) {
 // Few rows: 16 columns of C for up to 16 rows by NW waves that share the sum
 // among them, each taking every NW-th block of 128 straight from memory
 // (nothing is used twice), and add up in LDS in the order of the waves.  Bound
-// by the latency of the one or two loads that a wave has in turn: 16 x 2048 x
-// 8192 takes 12.8 us (13.1 with 16 waves), 16 x 8192 x 2048 6.9 us.
+// by latency: a wave has the loads of one block in flight (the compiler does
+// not unroll a loop of matrix instructions whose length it does not know), and
+// 2048 columns make 128 workgroups.  16 x 2048 x 8192 takes 12.8 us (13.1 with 16
+// waves), 16 x 8192 x 2048 6.9 us.
 template <int FA, int FB, bool WIDE, int NW>
 __global__ __launch_bounds__(64 * NW) void product_few_kernel(ProductArgs p) {
     __shared__ __attribute__((aligned(16))) float sums[NW][16 * 20];
@@ -532,7 +534,6 @@ __global__ __launch_bounds__(64 * NW) void product_few_kernel(ProductArgs p) {
     const uint8_t *qa = p.a + (uint64_t)ra * p.pitch + g * 32, *xa = p.sa + (uint64_t)ra * p.s_pitch;
     const uint8_t *qb = p.b + (uint64_t)rb * p.pitch + g * 32, *xb = p.sb + (uint64_t)rb * p.s_pitch;
     v4f acc[1][1] = {};
-#pragma unroll 4
     for (uint32_t kb = wave; kb < p.kb; kb += NW) {
         const uint32_t ea[1] = {xa[kb]}, eb[1] = {xb[kb]};
         const v8i fa[1] = {load_codes(qa + kb * kBlkK)}, fb[1] = {load_codes(qb + kb * kBlkK)};
@@ -574,7 +575,7 @@ __global__ __launch_bounds__(256) void product_rows_kernel(ProductArgs p) {
     if (j >= p.n) return;
     const uint8_t *qb = p.b + (uint64_t)j * p.pitch, *xb = p.sb + (uint64_t)j * p.s_pitch;
     float sum[M] = {};
-#pragma unroll(M == 1 ? 8 : 4)
+#pragma unroll M == 1 ? 8 : 4
     for (uint32_t k = lane * 16; k < p.pitch; k += 1024) {
         const v4i b = *(const v4i*)(qb + k);
         const int eb = xb[k >> 7];

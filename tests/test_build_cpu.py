@@ -49,3 +49,7 @@ def test_no_reserved_register_is_clobbered(warnings):
 
 def test_no_access_past_an_array(warnings):
     assert not [w for w in warnings if "array index" in w][:3]
+
+
+def test_no_warning_at_all(warnings):
+    assert not warnings[:3]
