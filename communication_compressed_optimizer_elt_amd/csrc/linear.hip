@@ -44,7 +44,7 @@ demo_operand operand_of(uint64_t rows, uint64_t cols) {
     return o;
 }
 
-// DropArgs of a configuration for n elements, or an error code
+// demo::Drop of a configuration for n elements, or an error code
 int drop_of(const demo_dropout_cfg* cfg, uint64_t n, demo::Drop* d) {
     *d = demo::Drop{};
     if (!cfg) return DEMO_OK;

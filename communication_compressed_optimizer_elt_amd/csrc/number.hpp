@@ -51,10 +51,6 @@ __device__ __forceinline__ void store8(T* p, const float (&v)[8]) {
 }
 
 // store8 past the caches
-__device__ __forceinline__ void stream8(float* p, const float (&v)[8]) {
-    __builtin_nontemporal_store(float4_v{v[0], v[1], v[2], v[3]}, (float4_v*)p);
-    __builtin_nontemporal_store(float4_v{v[4], v[5], v[6], v[7]}, (float4_v*)(p + 4));
-}
 template <typename T>
 __device__ __forceinline__ void stream8(T* p, const float (&v)[8]) {
     static_assert(sizeof(T) == 2, "two-byte type");
@@ -66,21 +62,6 @@ __device__ __forceinline__ void stream8(T* p, const float (&v)[8]) {
 }
 
 constexpr int kE4M3 = 0, kE5M2 = 1;
-
-// four 8-bit codes of four floats inside the format's range (NaN gives a NaN
-// code), the first in the low byte
-template <int FMT>
-__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
-    int w = 0;
-    if (FMT == kE4M3) {
-        w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, w, false);
-        w = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
-    } else {
-        w = __builtin_amdgcn_cvt_pk_bf8_f32(a, b, w, false);
-        w = __builtin_amdgcn_cvt_pk_bf8_f32(c, d, w, true);
-    }
-    return (uint32_t)w;
-}
 
 // Tile of workgroup `id`: the 8 XCDs, which take ids in turn, get runs of
 // neighbouring tiles each, and a run goes down kTileRun row tiles before it
