@@ -849,3 +849,16 @@ def test_product_in_16_bits_is_the_same_every_time(torch, out):
         for x in c:
             L.demo_block_matmul(L.Product(), m, n, k, a, b, x, workspace=ws)
         assert torch.equal(c[0], c[1]) and torch.equal(c[0], c[2])
+
+
+@pytest.mark.parametrize("m,n,k", PLANTED)
+def test_product_in_fp32_keeps_what_8_bit_instructions_lose(torch, m, n, k):
+    """448^2 - 448^2 + 2^-4 s: a sum kept to 2^-13 of 448^2 has none of it; 24
+    bits hold it (|448^2| < 2^18, everything a multiple of 2^-4)."""
+    va, vb = planted(m, n, k, 448.0, 0.25, 0.25)
+    a, b = (torch.from_numpy(F.pack(v, np.zeros((len(v), -(-k // 128)), np.int64), 0)).cuda() for v in (va, vb))
+    c = torch.full((m, n), float("nan"), device="cuda")
+    L.demo_block_matmul(L.Product(), m, n, k, a, b, c, workspace=workspace(torch, m, n, k))
+    want = torch.from_numpy(va).cuda() @ torch.from_numpy(vb).cuda().t().contiguous()
+    assert 13 + np.log2(0.25**2) < np.log2(448.0**2)  # lost at 13 places
+    assert (want != 0).any() and torch.equal(c.double(), want)
