@@ -862,3 +862,34 @@ def test_product_in_fp32_keeps_what_8_bit_instructions_lose(torch, m, n, k):
     want = torch.from_numpy(va).cuda() @ torch.from_numpy(vb).cuda().t().contiguous()
     assert 13 + np.log2(0.25**2) < np.log2(448.0**2)  # lost at 13 places
     assert (want != 0).any() and torch.equal(c.double(), want)
+
+
+@pytest.mark.parametrize("out", ["bf16", "f16"])
+@pytest.mark.parametrize("m", [1, 16, 40])
+def test_product_range_of_scales_in_16_bits(torch, m, out):
+    """Scale bytes far from 1, zero rows, overflow of the type, NaN codes."""
+    n, k = 48, 256
+    rng = np.random.default_rng(0)
+    va, vb = F.round_to(rng.standard_normal((m, k)), 0), F.round_to(rng.standard_normal((n, k)), 0)
+    ea, eb = np.zeros((m, 2), np.int64), np.zeros((n, 2), np.int64)
+    ea[0], eb[0] = 60, -60
+    eb[1] = 30
+    eb[3] = -20
+    eb[4, 0], eb[4, 1] = 20, -20
+    vb[5], eb[5] = 0, -127
+    if m > 5:
+        ea[1], ea[4, 0], ea[4, 1] = -60, 20, -20
+        va[2], ea[2] = 0, -127
+    a, b = F.pack(va, ea, 0), F.pack(vb, eb, 0)
+    pitch = F.layout(m, k)[0]
+    if m > 7:
+        a[7 * pitch + 130] = 0x7F
+    b[9 * pitch + 5] = 0xFF
+    c = torch.empty(m, n, dtype=dt(torch, out), device="cuda")
+    L.demo_block_matmul(L.Product(), m, n, k, torch.from_numpy(a).cuda(), torch.from_numpy(b).cuda(), c,
+                        workspace=workspace(torch, m, n, k))
+    want_nan = torch.zeros(m, n, dtype=torch.bool)
+    want_nan[7:8], want_nan[:, 9] = True, True
+    assert torch.equal(torch.isnan(c.cpu()), want_nan)
+    rows, cols = [i for i in range(m) if i != 7], [j for j in range(n) if j != 9]
+    check_product(torch, c.cpu()[rows][:, cols], F.value(va, ea)[rows], F.value(vb, eb)[cols])
