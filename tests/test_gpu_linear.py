@@ -893,3 +893,69 @@ def test_product_range_of_scales_in_16_bits(torch, m, out):
     assert torch.equal(torch.isnan(c.cpu()), want_nan)
     rows, cols = [i for i in range(m) if i != 7], [j for j in range(n) if j != 9]
     check_product(torch, c.cpu()[rows][:, cols], F.value(va, ea)[rows], F.value(vb, eb)[cols])
+
+
+# ------------------------------------------------ quantiser, 16-bit sources --
+
+def edges_of_16_bits(torch, dtype):
+    """Rows of 256 columns: block maxima next to powers of two and to 1.75
+    times one over the type's whole range, in either half of a pair, with
+    values below them down to what underflows; subnormals only; the type's
+    largest and smallest values; zeros of both signs."""
+    f = torch.finfo(dtype)
+    low, top, eps = int(np.log2(f.tiny)) + int(np.log2(f.eps)), int(np.floor(np.log2(f.max))), f.eps
+    rows = []
+    for e in sorted({low, low + 1, low + 3, low - int(np.log2(eps)) - 1, low - int(np.log2(eps)), -9, -1, 0, 8, 9, top - 1, top}):
+        for i, m in enumerate((1.0, 1.0 + eps, 1.75, 1.75 + eps, 2.0 - eps)):
+            x = np.ldexp(m, e)
+            row = np.array([x * 2.0**-j * s for j in range(64) for s in (1, -0.75)] * 2)
+            row[128:] *= -1
+            rows.append(np.roll(row, i))
+    sub = np.arange(256.0) % 120 + 1  # whole multiples of the smallest subnormal
+    rows += [sub * 2.0**low, -sub[::-1] * 2.0**low * (np.arange(256) % 2), np.zeros(256), -np.zeros(256)]
+    for at, v in ((0, f.max), (1, -f.max), (254, 2.0**low), (255, -(2.0**low))):
+        row = np.zeros(256)
+        row[at] = row[(at + 128) % 256] = v
+        rows.append(row)
+    return torch.from_numpy(np.array(rows)).to(dtype).cuda()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("tile", [0, 1])
+@pytest.mark.parametrize("cols", [256, 251])
+def test_quantize_edges_of_16_bit_types(torch, dtype, fmt, tile, cols):
+    x = edges_of_16_bits(torch, dt(torch, dtype))[:, :cols].contiguous()
+    x = torch.cat([x, x.flip(0)])  # more than one square down
+    q, qt = operand(torch, *x.shape), operand(torch, x.shape[1], x.shape[0])
+    L.demo_block_quantize(L.Block(fmt=fmt, tile=tile), x, q, qt)
+    check_operand(torch, q, host(x), fmt, tile)
+    check_operand(torch, qt, host(x).T, fmt, tile)
+    small = x[: x.shape[0] // 2] * 0  # nothing but subnormals in a whole square
+    small[::3] = x[x.shape[0] // 2 - 8]
+    q, qt = operand(torch, *small.shape), operand(torch, small.shape[1], small.shape[0])
+    L.demo_block_quantize(L.Block(fmt=fmt, tile=tile), small, q, qt)
+    check_operand(torch, q, host(small), fmt, tile)
+    check_operand(torch, qt, host(small).T, fmt, tile)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("tile", [0, 1])
+@pytest.mark.parametrize("cols", [304, 301])
+def test_quantize_infinities_and_nan_of_16_bit_types(torch, dtype, fmt, tile, cols):
+    x = normal(torch, 9, 200, cols, dtype=dt(torch, dtype))
+    inf, nan = float("inf"), float("nan")
+    x[3, 5], x[3, 200], x[150, 20], x[199, cols - 1], x[150, 21], x[151, 20] = inf, nan, -inf, nan, inf, -nan
+    x[7] = nan  # blocks of nothing but NaN, and of nothing but infinities
+    x[8, :128], x[9, 128:256] = inf, -inf
+    x[:128, 40], x[128:, 41] = nan, inf
+    x[20, ::2], x[21, 1::2] = nan, inf
+    q, qt = operand(torch, 200, cols), operand(torch, cols, 200)
+    L.demo_block_quantize(L.Block(fmt=fmt, tile=tile), x, q, qt)
+    check_operand(torch, q, host(x), fmt, tile)
+    check_operand(torch, qt, host(x).T, fmt, tile)
+    x[:128, :128] = nan  # a whole square
+    L.demo_block_quantize(L.Block(fmt=fmt, tile=tile), x, q, qt)
+    check_operand(torch, q, host(x), fmt, tile)
+    check_operand(torch, qt, host(x).T, fmt, tile)
