@@ -959,3 +959,26 @@ def test_quantize_infinities_and_nan_of_16_bit_types(torch, dtype, fmt, tile, co
     L.demo_block_quantize(L.Block(fmt=fmt, tile=tile), x, q, qt)
     check_operand(torch, q, host(x), fmt, tile)
     check_operand(torch, qt, host(x).T, fmt, tile)
+
+
+@pytest.mark.parametrize("p", [0.0, 0.2, 1.0 - 2.0**-16, 1.0])
+@pytest.mark.parametrize("dtype", sorted(DT))
+@pytest.mark.parametrize("tile", [0, 1])
+@pytest.mark.parametrize("rows,cols", [(130, 256), (129, 131), (3, 5)])
+def test_quantize_to_e4m3_with_dropout(torch, rows, cols, tile, dtype, p):
+    """As test_quantize_with_dropout and its range's end, in the other format."""
+    x = normal(torch, 10, rows, cols, dtype=dt(torch, dtype))
+    top = torch.finfo(x.dtype).max
+    x[0, 0] = float("nan")
+    x[1::9, ::5] = top
+    x[2::9, 1::7] = -top / 1.99
+    x[2, 4] = float("inf")
+    x[5::9] *= torch.finfo(x.dtype).tiny
+    kw = dict(p=p, seed=77, step=3, site=2, chunk_offset=9)
+    q, qt = operand(torch, rows, cols), operand(torch, cols, rows)
+    L.demo_block_quantize(L.Block(fmt=0, tile=tile), x, q, qt, dropout=L.Dropout(**kw))
+    with np.errstate(over="ignore", invalid="ignore"):
+        g = np.float32(host(x)) * np.float32(F.scale(p))  # fp32, rounded once
+    g = np.where(F.keep(rows * cols, **kw).reshape(rows, cols), g, np.float32(0))
+    check_operand(torch, q, g, 0, tile)
+    check_operand(torch, qt, g.T, 0, tile)
