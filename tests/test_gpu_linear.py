@@ -982,3 +982,40 @@ def test_quantize_to_e4m3_with_dropout(torch, rows, cols, tile, dtype, p):
     g = np.where(F.keep(rows * cols, **kw).reshape(rows, cols), g, np.float32(0))
     check_operand(torch, q, g, 0, tile)
     check_operand(torch, qt, g.T, 0, tile)
+
+
+def test_two_graphs_at_the_same_time(torch):
+    """Two captured layers with workspaces of their own, replayed on two streams
+    without a wait between them: every output as the eager run's."""
+    made = []
+    for i, (tokens, n, k) in enumerate(((512, 512, 2048), (500, 768, 1024))):
+        layer = Layer(torch, normal(torch, i, n, k, std=0.05), L.Dropout(p=0.1, seed=i), tokens, torch.zeros(n, k, device="cuda"))
+        x, dy = (normal(torch, 10 + i, tokens, c, dtype=torch.bfloat16) for c in (k, n))
+        res, y, dx = torch.zeros_like(dy), torch.empty_like(dy), torch.empty_like(x)
+
+        def step(layer=layer, x=x, dy=dy, res=res, y=y, dx=dx):
+            layer.take_weight()
+            layer.forward(x, res, y)
+            layer.grad.zero_()
+            layer.backward(dy, dx)
+
+        step()
+        torch.cuda.synchronize()
+        outs = (y, dx, layer.grad)
+        want = [o.clone() for o in outs]
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step()
+        made.append((graph, torch.cuda.Stream(), outs, want, step))  # step holds what the graph reads
+    for rep in range(4):
+        for _, _, outs, _, _ in made:
+            for o in outs:
+                o.fill_(7.0)
+        torch.cuda.synchronize()
+        for _ in range(3):
+            for graph, stream, _, _, _ in made:
+                with torch.cuda.stream(stream):
+                    graph.replay()
+        torch.cuda.synchronize()
+        for _, _, outs, want, _ in made:
+            assert all(torch.equal(a, b) for a, b in zip(outs, want)), rep
