@@ -148,8 +148,8 @@ struct Plan {
     uint32_t kb_split;
 };
 
-// The card runs 256 tiles of 256 x 256 at a time, or 512 of 128 x 128 or 64 x
-// 64 (two workgroups a CU).  Measured, 16-bit result:
+// The card runs 256 tiles of 256 x 256 at a time, 512 of 128 x 128 or 1024 of 64
+// x 64 (one, two and four workgroups a CU).  Measured, 16-bit result:
 //  * a round of 256 tiles costs 1.6 to 1.8 rounds of 128 tiles (8192 x 2048 x
 //    2048: 32.2 against 38.3 us; 6144 x 4096 x 2048, where the second round is
 //    half empty: 56.3 against 53.9 us; 4096 x 2048 x 2048, half a round: 25.6
@@ -159,10 +159,14 @@ struct Plan {
 //    us, 24.1 against 28.7 us with an fp32 result); 16-bit results with a sum of
 //    8192 or more up to 192 (2048 x 2048 x 8192: 54 against 53 us, but 75 against
 //    85 us with an fp32 result);
-//  * the sum is split where tiles fill less than a round: down to 16 blocks of
-//    128 for tiles of 64 (256 x 2048 x 8192: 16.4 us in 4, 23.8 in one; 128 x
-//    2048 x 2048: 7.6 us in one, 9.7 in 2), to 64 for tiles of 128 (2048 x 2048
-//    x 16384: 80 us in 2, 90 in one).
+//  * the sum is split where there are fewer than 512 workgroups: down to 16
+//    blocks of 128 for tiles of 64 (256 x 2048 x 8192: 16.4 us in 4, 23.8 in one;
+//    128 x 2048 x 2048: 7.6 us in one, 9.7 in 2), to 64 for tiles of 128 (2048 x
+//    2048 x 16384: 80 us in 2, 90 in one).  Up to 1024 workgroups, which tiles of
+//    64 would fill, measured no better: 512 x 2048 x 8192 23.7 us in 4, 23.9 in 2
+//    (fp32 result: 28.9 and 26.6); 768 x 768 x 16384 28.0 us in 7, 29.8 in 3
+//    (33.2 and 31.7).  Nor did 8 blocks: 256 x 2048 x 2048 11.6 us in 2, 10.1 in
+//    one; 256 x 2048 x 8192 18.5 us in 8, 16.7 in 4.
 // With an fp32 result a round of 256 tiles costs 1.75 to 1.87 of 128 (8192 x
 // 8192 x 8192: 890 against 969 us; 4096 x 8192 x 2048: 148 against 158 us).
 Plan plan_of(uint64_t m, uint64_t n, uint64_t k, bool wide) {
