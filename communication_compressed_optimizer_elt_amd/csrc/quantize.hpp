@@ -15,13 +15,25 @@
 // sources stay pairs of 16 bits, whose magnitudes compare as integers, until
 // the hardware's scaled conversion makes codes of them.
 //
-// Bound by memory: 16384 x 8192 bf16 to e4m3, both operands (537 MB), takes 99
-// us (5.4 TB/s; 112 us before the pieces of a transposed row were written side
-// by side and the source read past the caches); 8192 x 2048 fp32 in squares
-// (101 MB) 24 us and 16384 x 2048 bf16 through a dropout to e5m2 (134 MB) 36 us,
-// one or two rounds of workgroups whose loads, arithmetic and stores coincide.
-// Workgroups that stay and load their next square early spilled and took twice
-// as long (54 us for the fp32 weight).
+// Bound by memory where it is large: 16384 x 8192 bf16 to e4m3, both operands
+// (537 MB), takes 99 us in a layer (5.4 TB/s; 112 us before the pieces of a
+// transposed row were written side by side and the source read past the
+// caches), 112 to 121 us back to back.  8192 x 2048 fp32 in squares (101 MB) takes
+// 24 us and 16384 x 2048 bf16 through a dropout to e5m2 (134 MB) 36 us, one or
+// two rounds of workgroups whose loads, arithmetic and stores coincide: waves
+// wait to issue for 62% and 45% of their time.  Workgroups that stay and load
+// their next square early spilled for fp32 sources, 64 registers a square, and
+// took twice as long (54 us for the weight); 16-bit squares are 32 registers of
+// 83 (106 with a dropout) and have not been tried so.  2561 x 768 bf16 takes 7.1
+// us: its 126 workgroups leave half of the CUs idle, and a wave's load, maxima,
+// exchange and store follow one another.
+//
+// Sources of odd width or pitch are read value by value: 16384 x 8191 bf16 212
+// us, 8192 x 2047 fp32 in squares 42 us, 16384 x 2047 bf16 through a dropout 71
+// us.  The fp32 kernels spill 57 to 76 scalar registers to lanes of vector
+// registers, most of them on the path for infinities and NaN; those with a
+// dropout on such sources also 8 to 10 vector registers to scratch (16384 x 2047:
+// 86 us against 54 us of 2048 columns, 21 MB written on top).
 #pragma once
 
 #include <type_traits>
