@@ -83,8 +83,8 @@ struct DropoutArgs {
 // dropped element is not read into the result, so NaN or infinity there leaves
 // no trace.  One work-item per Philox block, whose eight bf16 values are one
 // 16-byte access.  Bound by memory: the gradient of 16384 x 8192 bf16 takes 88
-// us (6.1 TB/s); 2561 x 768 fp32 with a residual 5.9 us, 16 x 2048 bf16 2.6 us,
-// which is the launch.
+// us (6.1 TB/s); 2561 x 768 fp32 with a residual 5.2 to 6.2 us, 16 x 2048 bf16 2.2
+// to 2.6 us, which is the launch.
 template <typename T, bool RES>
 __global__ __launch_bounds__(256) void dropout_kernel(DropoutArgs p) {
     const T* x = (const T*)p.x;

@@ -409,7 +409,9 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(ProductArgs p) {
 // operands for its 16 matrix instructions, half of what it would widen for 32 x
 // 32 of C and the whole block: 2304 x 768 x 2560 takes 17.2 us (18.8 so), 2048 x
 // 2048 x 8192 75 us (85 so).  Bound by issue: widening and matrix instructions
-// of a SIMD's waves take turns; two blocks a barrier gave nothing (19.4 against
+// of a SIMD's waves take turns (six VALU instructions for each matrix one, whose
+// units are busy for 28% of the time), on 432 tiles that the CUs share unevenly;
+// two blocks a barrier gave nothing (19.4 against
 // 18.4 us with an addend).  Loads, stages and chunks as in product_kernel.  In
 // the end wave w takes rows 16 w .. +15 and adds the others' sums in the order
 // w, w+3, w+2, w+1 (mod 4): three exchanges through two halves of LDS.
@@ -523,8 +525,9 @@ __device__ __forceinline__ v8i load_codes(const uint8_t* p) {
 // (nothing is used twice), and add up in LDS in the order of the waves.  Bound
 // by latency: a wave has the loads of one block in flight (the compiler does
 // not unroll a loop of matrix instructions whose length it does not know), and
-// 2048 columns make 128 workgroups.  16 x 2048 x 8192 takes 12.8 us (13.1 with 16
-// waves), 16 x 8192 x 2048 6.9 us.
+// 2048 columns make 128 workgroups: waves wait for 95% of their time.  16 x 2048
+// x 8192 takes 12.2 to 13.2 us (13.1 with 16 waves where it took 12.8), 16 x 8192
+// x 2048 6.9 to 7.6 us.
 template <int FA, int FB, bool WIDE, int NW>
 __global__ __launch_bounds__(64 * NW) void product_few_kernel(ProductArgs p) {
     __shared__ __attribute__((aligned(16))) float sums[NW][16 * 20];
@@ -565,7 +568,8 @@ __device__ __forceinline__ void floats2(uint32_t w, float& x, float& y) {
 // C, its lanes along the sum, 16 codes each, in fp32; the eight lanes of a
 // block of 128 scale what they have of it.  No matrix instruction, whose other
 // 15 rows would be empty: one row x 2048 x 8192 takes 5.8 us against 8.5 us of
-// product_few_kernel, 16384 x 8192 24.7 against 29.7 us (5.4 TB/s of codes);
+// product_few_kernel beside it (6.0 to 6.4 us with inputs that no cache holds),
+// 16384 x 8192 24.7 against 29.7 us (5.4 TB/s of codes);
 // two rows 6.1 against 9.0 us; at four rows the gain is gone (8.2, 9.7 us, and
 // 7.3 against 5.4 us with 8192 columns of 2048).
 template <int FA, int FB, int M>

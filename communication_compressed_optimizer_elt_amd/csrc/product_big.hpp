@@ -107,12 +107,16 @@ __device__ __forceinline__ void settle() {
 // flight, one and a half blocks ahead of their use.
 //
 // Bound by the matrix instructions at the clock that their power leaves (3.8
-// PFLOP/s on random codes in registers, 4.7 on constant ones), and by the
-// results that all CUs write at the same time between two tiles: 8192 x 8192 x
-// 8192 takes 375 to 400 us (2.75 to 2.93 PFLOP/s), 4096 x 8192 x 2048 61 us,
-// 2048 x 100352 x 2048 368 to 385 us.  Loading the next tile's first blocks
-// before the way out gave nothing (77.4 against 78.4 us), nor did two groups of
-// 4 waves out of step (494 against 464 us).
+// PFLOP/s on random codes in registers, 4.7 on constant ones; 1.9 of 2.4 GHz
+// here) for long sums, where their units are busy for 74% of the time, and for
+// sums of 2048, where it is 50%, as much by a tile's first loads and by the
+// results that all CUs write at the same time between two tiles.  Over cards and
+// runs 8192 x 8192 x 8192 takes 375 to 425 us (2.59 to 2.93 PFLOP/s), 4096 x 8192
+// x 2048 60 to 65 us, 2048 x 100352 x 2048 368 to 422 us; columns that are no
+// multiple of 8 are stored one by one (2048 x 50257 x 2048 331 us, 50256 220 us).
+// Loading the next tile's first blocks before the way out gave nothing (77.4
+// against 78.4 us), nor did two groups of 4 waves out of step (494 against 464
+// us).
 template <int FA, int FB>
 __global__ __launch_bounds__(256, 1) void product_big_kernel(ProductArgs p) {
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
@@ -251,7 +255,8 @@ __global__ __launch_bounds__(256, 1) void product_big_kernel(ProductArgs p) {
 // four waves before they widen the last step's codes and the others after.
 // Behind it the next block has landed, nobody reads this block's stage again,
 // and the loads of the block after the next go there.  8192 x 8192 x 8192 takes
-// 890 us (1.24 PFLOP/s), in tiles of 128 969 us on the same card.
+// 844 to 890 us (1.24 to 1.30 PFLOP/s), in tiles of 128 969 us on the card of the
+// 890; the matrix units are busy for 68% of it.
 typedef float v16f __attribute__((ext_vector_type(16)));
 __device__ __forceinline__ void mma16(v16f& d, const v8b& a, const v8b& b) {
     asm volatile("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+a"(d) : "v"(a), "v"(b));
