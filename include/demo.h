@@ -349,15 +349,17 @@ int demo_block_workspace(const demo_product_cfg *cfg, uint64_t m, uint64_t n, ui
  * the result's, that is 1.5e-5 on normal values and up to 4.7e-5 where a few
  * channels are 20 times larger: at most 1/35 of the rounding to bf16, but 1/14
  * to 1/4 of the rounding to fp16.  An fp32 result is the way to have it exact.
- * addend may be NULL, or c itself with
- * the same pitch (to add to a gradient); dropout (NULL: none) applies to the
- * product as demo_dropout does, element i*n + j.  c and addend [m][n] with row
- * pitches ldc and ld_addend in elements, aligned to their element, (m - 1)*ldc
- * and (m - 1)*ld_addend at most 2^40.  m, n at most 2^30, k at most
- * DEMO_BLOCK_MAX_K (DEMO_EUNSUPPORTED beyond), each of m*n, m*k and n*k at most
- * DEMO_MAX_ELEMS.  The workspace is written by the call and free again when it
- * has run: calls that may run at the same time (other streams, other graphs)
- * need one each.
+ * addend may be NULL, or c itself with the same pitch (to add to a gradient);
+ * dropout (NULL: none) applies to the product as demo_dropout does, element
+ * i*n + j.  c and addend [m][n] with row pitches ldc and ld_addend in elements,
+ * aligned to their element, (m - 1)*ldc and (m - 1)*ld_addend at most 2^40.
+ * m, n at most 2^30, k at most DEMO_BLOCK_MAX_K (DEMO_EUNSUPPORTED beyond), each
+ * of m*n, m*k and n*k at most DEMO_MAX_ELEMS.  c, from its first element to its
+ * last with what lies between its rows, may overlap no other buffer of the
+ * call, so neighbouring column slices of one matrix cannot be c and addend;
+ * the workspace neither.  The workspace is written by the call and free again
+ * when it has run: calls that may run at the same time (other streams, other
+ * graphs) need one each.
  */
 int demo_block_matmul(const demo_product_cfg *cfg, uint64_t m, uint64_t n, uint64_t k, const void *a, const void *b,
                       void *c, uint64_t ldc, const void *addend, uint64_t ld_addend,

@@ -124,6 +124,13 @@ def test_matmul_refusals():
     assert call(addend=3 * FAR, ld_addend=128) == L.EINVAL  # c with another pitch
 
 
+def test_matmul_refuses_slices_of_one_matrix():
+    """Columns 0..95 of a matrix of 192 as c, 96..191 as addend: their spans overlap."""
+    args = (L.Product().c(L.DTYPE_F32), 64, 96, 300, FAR, 2 * FAR)
+    assert L.raw_block_matmul(*args, 3 * FAR, 192, addend=3 * FAR + 4 * 96, ld_addend=192) == L.EINVAL
+    assert L.raw_block_matmul(*args, 3 * FAR + 4 * 96, 192, addend=3 * FAR, ld_addend=192) == L.EINVAL
+
+
 def test_workspace_sizes():
     for m, n, k in ((1, 2048, 8192), (2304, 768, 2561), (4096, 8192, 2048), (768, 768, 1 << 22), (64, 64, 1 << 22)):
         rc, need = L.raw_block_workspace(L.Product().c(), m, n, k)
