@@ -3,8 +3,8 @@
 Every computation runs in the HIP kernels of libdemo.so; this module turns
 PyTorch tensors into device pointers and the current HIP stream, checks that
 each tensor is a contiguous device tensor of the dtype and size the call
-reads or writes (so no kernel can run past it), and raises on error codes.  There is no fallback: if libdemo.so is missing the first call
-raises.
+reads or writes (so no kernel can run past it), and raises on error codes.
+There is no fallback: if libdemo.so is missing the first call raises.
 """
 from __future__ import annotations
 
@@ -177,6 +177,12 @@ def lib() -> ctypes.CDLL:
     if _lib is None:
         if not os.path.exists(LIB_PATH):
             raise RuntimeError(f"{LIB_PATH} is not built (run __graft_entry__.build())")
+        # torch brings a HIP runtime of its own: loaded first, libdemo binds to it;
+        # loaded second, there would be two, and no launch on torch's streams works
+        try:
+            import torch  # noqa: F401
+        except ImportError:  # raw addresses and the calls that need no GPU
+            pass
         L = ctypes.CDLL(LIB_PATH)
         P = ctypes.c_void_p
         L.demo_abi_version.argtypes = []
