@@ -22,6 +22,7 @@ import argparse
 import hashlib
 import json
 import os
+import struct
 import sys
 import time
 from dataclasses import dataclass
@@ -34,6 +35,7 @@ sys.path.insert(0, ROOT)
 HBM_PEAK_GBPS = 8000.0  # MI355X HBM3E, AMD's published figure
 METRIC = "params/s and HBM GB/s (% of peak) of DeMo encode+decode, OLMo2-1B half shard"
 DILOCO_PERIOD = 16
+BUNDLE_MAGIC = b"__CLANG_OFFLOAD_BUNDLE__"
 
 
 @dataclass(frozen=True)
@@ -76,14 +78,11 @@ WORKLOADS = {
 LAUNCH_BOUND = {"tensor-4096-demo-k4"}
 
 
-def _elf_section(path: str, wanted: str) -> bytes:
+def _elf_section(data: bytes, wanted: str) -> bytes:
     """Bytes of one section of a 64-bit little-endian ELF file (our own build)."""
-    import struct
-
-    with open(path, "rb") as f:
-        data = f.read()
     shoff, = struct.unpack_from("<Q", data, 0x28)
     shentsize, shnum, shstrndx = struct.unpack_from("<HHH", data, 0x3A)
+
     def header(i):
         name, _, _, _, off, size = struct.unpack_from("<IIQQQQ", data, shoff + i * shentsize)
         return name, off, size
@@ -96,13 +95,36 @@ def _elf_section(path: str, wanted: str) -> bytes:
     raise KeyError(wanted)
 
 
+def _step_code_object(library: bytes) -> bytes:
+    """The GPU code object of the library that holds the optimizer step's
+    kernels: the library has one for each source file, each in an offload
+    bundle of its own."""
+    fat = _elf_section(library, ".hip_fatbin")
+    bundle = fat.find(BUNDLE_MAGIC)
+    while bundle >= 0:
+        count, = struct.unpack_from("<Q", fat, bundle + len(BUNDLE_MAGIC))
+        at = bundle + len(BUNDLE_MAGIC) + 8
+        for _ in range(count):
+            off, size, name_len = struct.unpack_from("<QQQ", fat, at)
+            at += 24 + name_len
+            code = fat[bundle + off:bundle + off + size]
+            if b"encode_dct_kernel" in code:
+                return code
+        bundle = fat.find(BUNDLE_MAGIC, bundle + 1)
+    raise KeyError("encode_dct_kernel")
+
+
 def library_hash() -> str:
-    """SHA-256 prefix of the device code in the built libdemo.so (its .hip_fatbin
-    section): a traffic record taken with rocprofv3 applies only to the exact
-    kernels it measured; host-side and comment-only changes keep the hash."""
+    """SHA-256 prefix of the optimizer step's device code in the built
+    libdemo.so, instructions and kernel descriptors: a traffic record taken
+    with rocprofv3 applies only to the exact kernels it measured; host-side and
+    comment-only changes, the library's other operators and the folder it is
+    built in keep the hash."""
     from communication_compressed_optimizer_elt_amd import binding
 
-    return hashlib.sha256(_elf_section(binding.LIB_PATH, ".hip_fatbin")).hexdigest()[:16]
+    with open(binding.LIB_PATH, "rb") as f:
+        code = _step_code_object(f.read())
+    return hashlib.sha256(_elf_section(code, ".text") + _elf_section(code, ".rodata")).hexdigest()[:16]
 
 
 class Inputs:

@@ -101,3 +101,11 @@ def test_traffic_records_match_the_benchmark_accounting(lib):
             expect = (12 if w.adamw else 8) * n + w.R * pb
         assert abs(rec["algorithmic_bytes_per_launch"] - expect) <= 1e-9 * expect, (f, expect)
         assert 0.99 <= rec["hbm_bytes_per_launch"] / rec["algorithmic_bytes_per_launch"] <= 1.01, f
+
+
+@pytest.mark.parametrize("kind", ["encode", "decode"])
+def test_traffic_records_of_the_default_workload_are_of_the_built_kernels(lib, kind):
+    """The benchmark's line has a traffic figure only from a record of the
+    kernels as built; other operators in the library take nothing from it."""
+    rec = json.load(open(os.path.join(ROOT, "profiles", f"traffic_{kind}_olmo2-1b-half-shard-demo-k1.json")))
+    assert rec["library_hash"] == bench.library_hash()
