@@ -258,7 +258,10 @@ enum { DEMO_FMT_E4M3 = 0, DEMO_FMT_E5M2 = 1 };
  * that number is at least T = floor(65536 p + 1/2); kept values are scaled by
  * 65536/(65536 - T) in fp32 (0 for T = 65536).  A shard that starts at
  * chunk_offset draws what the whole tensor draws there, and no draw of
- * demo_random_select with the same seed coincides with one of these.
+ * demo_random_select with the same seed coincides with one of these.  The
+ * configuration is read when the call is made: a call captured in a graph draws
+ * the numbers of that step at every replay, so a graph that is replayed for
+ * step after step has its dropouts outside, or is captured anew.
  */
 typedef struct demo_dropout_cfg {
     uint32_t abi_version;  /* must be DEMO_ABI_VERSION */

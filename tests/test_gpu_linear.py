@@ -1019,3 +1019,26 @@ def test_two_graphs_at_the_same_time(torch):
         torch.cuda.synchronize()
         for _, _, outs, want, _ in made:
             assert all(torch.equal(a, b) for a, b in zip(outs, want)), rep
+
+
+def test_a_captured_dropout_draws_its_step_at_every_replay(torch):
+    """The configuration is read when the call is made; the backward pass of
+    that step, made later and eagerly, draws the same numbers."""
+    n = 5000
+    x, d = torch.ones(n, device="cuda"), L.Dropout(p=0.5, seed=4, step=10)
+    y, dx = torch.empty_like(x), torch.empty_like(x)
+    L.demo_dropout(d, x, y)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        L.demo_dropout(d, x, y)
+    want = torch.from_numpy(F.keep(n, 0.5, seed=4, step=10)).cuda() * 2.0
+    for step in (11, 12, 13):
+        d.step = step
+        y.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want.float())
+    d.step = 10
+    L.demo_dropout_backward(d, x, dx)
+    assert torch.equal(dx, y)
