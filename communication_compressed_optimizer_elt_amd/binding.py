@@ -25,12 +25,18 @@ FMT_E4M3, FMT_E5M2 = 0, 1
 BLOCK = 128
 BLOCK_MAX_K = 1 << 22
 BLOCK_MAX_WORKSPACE = 64 << 20
+NORM_MAX_COLS = 16384
+MAX_TENSORS = 65536
+MX_BLOCK = 32
 OK, EINVAL, EALIGN, EUNSUPPORTED, EHIP, EABI = 0, -1, -2, -3, -4, -5
 
 SYMBOLS = ("demo_abi_version", "demo_strerror", "demo_payload_layout", "demo_encode",
            "demo_decode_apply", "demo_random_select", "demo_encode_adamw", "demo_decode_apply_adamw",
            "demo_payload_validate", "demo_dropout", "demo_dropout_backward", "demo_block_layout",
-           "demo_block_quantize", "demo_block_workspace", "demo_block_matmul")
+           "demo_block_quantize", "demo_block_workspace", "demo_block_matmul", "demo_rms_norm",
+           "demo_rms_norm_workspace", "demo_rms_norm_backward", "demo_grad_workspace", "demo_grad_norm",
+           "demo_grad_clip", "demo_mx_layout", "demo_mx_quantize", "demo_mx_dequantize", "demo_mx_workspace",
+           "demo_mx_matmul")
 
 
 class DemoError(RuntimeError):
@@ -91,6 +97,20 @@ class demo_product_cfg(ctypes.Structure):
     _fields_ = [(n, ctypes.c_uint32) for n in ("abi_version", "fmt_a", "fmt_b", "dtype")]
 
 
+class demo_norm_cfg(ctypes.Structure):
+    _fields_ = [("abi_version", ctypes.c_uint32), ("dtype", ctypes.c_uint32), ("fmt", ctypes.c_uint32),
+                ("eps", ctypes.c_float)]
+
+
+class demo_tensor(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("n_elems", ctypes.c_uint64), ("dtype", ctypes.c_uint32),
+                ("reserved", ctypes.c_uint32)]
+
+
+class demo_mx_cfg(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_uint32) for n in ("abi_version", "tile", "dtype", "reserved")]
+
+
 @dataclass
 class Dropout:
     """Python view of demo_dropout_cfg."""
@@ -130,6 +150,30 @@ class Product:
 
     def c(self, dtype: int = DTYPE_F32) -> demo_product_cfg:
         return demo_product_cfg(self.abi_version, self.fmt_a, self.fmt_b, dtype)
+
+
+@dataclass
+class Norm:
+    """Python view of demo_norm_cfg; the matrices' type comes from the tensors."""
+
+    eps: float = 1e-6
+    fmt: int = FMT_E4M3
+    abi_version: int = ABI_VERSION
+
+    def c(self, dtype: int = DTYPE_F32) -> demo_norm_cfg:
+        return demo_norm_cfg(self.abi_version, dtype, self.fmt, self.eps)
+
+
+@dataclass
+class Mx:
+    """Python view of demo_mx_cfg; the matrix' type comes from the tensor."""
+
+    tile: int = 0
+    abi_version: int = ABI_VERSION
+    reserved: int = 0
+
+    def c(self, dtype: int = DTYPE_F32) -> demo_mx_cfg:
+        return demo_mx_cfg(self.abi_version, self.tile, dtype, self.reserved)
 
 
 @dataclass
@@ -215,8 +259,20 @@ def lib() -> ctypes.CDLL:
         L.demo_block_quantize.argtypes = [ctypes.POINTER(demo_block_cfg), U64, U64, P, U64, drop, P, P, P]
         L.demo_block_workspace.argtypes = [prod, U64, U64, U64, ctypes.POINTER(U64)]
         L.demo_block_matmul.argtypes = [prod, U64, U64, U64, P, P, P, U64, P, U64, drop, P, U64, P]
-        for name in ("demo_dropout", "demo_dropout_backward", "demo_block_layout", "demo_block_quantize",
-                     "demo_block_workspace", "demo_block_matmul"):
+        norm, mx = ctypes.POINTER(demo_norm_cfg), ctypes.POINTER(demo_mx_cfg)
+        tensors = ctypes.POINTER(demo_tensor)
+        L.demo_rms_norm.argtypes = [norm, U64, U64, P, U64, P, U64, P, P, U64, P, U64, P, P, P, P]
+        L.demo_rms_norm_workspace.argtypes = [norm, U64, U64, ctypes.POINTER(U64)]
+        L.demo_rms_norm_backward.argtypes = [norm, U64, U64, P, U64, P, U64, P, P, P, U64, P, U64, P, P, P, U64, P]
+        L.demo_grad_workspace.argtypes = [U32, tensors, ctypes.POINTER(U64)]
+        L.demo_grad_norm.argtypes = [U32, tensors, P, P, U64, P]
+        L.demo_grad_clip.argtypes = [U32, tensors, tensors, P, ctypes.c_float, P, P]
+        L.demo_mx_layout.argtypes = [U64, U64, ctypes.POINTER(demo_operand)]
+        L.demo_mx_quantize.argtypes = [mx, U64, U64, P, U64, drop, P, P, P]
+        L.demo_mx_dequantize.argtypes = [mx, U64, U64, P, P, U64, P]
+        L.demo_mx_workspace.argtypes = [mx, U64, U64, U64, ctypes.POINTER(U64)]
+        L.demo_mx_matmul.argtypes = [mx, U64, U64, U64, P, P, P, U64, P, U64, drop, P, U64, P]
+        for name in SYMBOLS[SYMBOLS.index("demo_dropout"):]:
             getattr(L, name).restype = ctypes.c_int
         if L.demo_abi_version() != ABI_VERSION:
             raise RuntimeError("libdemo.so ABI version mismatch")
@@ -513,6 +569,227 @@ def demo_block_matmul(cfg, m: int, n: int, k: int, a, b, c, addend=None, dropout
                                    _stream(stream, dev)), "demo_block_matmul")
 
 
+def _vector(t, what: str, dev: int, n: int) -> int | None:
+    """Address of a contiguous fp32 vector of n elements on device dev."""
+    if t is None:
+        return None
+    if t.get_device() != dev:
+        _here(t, what)
+    if not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous tensor")
+    if _dtype(t, what) != DTYPE_F32:
+        raise TypeError(f"{what}: expected float32, got {t.dtype}")
+    if t.numel() != n:
+        raise ValueError(f"{what}: holds {t.numel()} elements, not {n}")
+    return t.data_ptr()
+
+
+def _maybe_matrix(t, what: str, dev: int, like) -> tuple[int | None, int]:
+    return (None, 0) if t is None else _matrix(t, what, dev, tuple(like.shape), like.dtype)
+
+
+def _workspace(t, dev: int) -> tuple[int | None, int]:
+    if t is None:
+        return None, 0
+    if t.get_device() != dev:
+        _here(t, "workspace")
+    return _buf(t, "workspace", 0), t.numel() * t.element_size()
+
+
+def demo_rms_norm(cfg, x, weight, y=None, residual=None, h=None, rstd=None, operand=None, operand_t=None,
+                  stream=None) -> None:
+    """h = residual + x, y = h / rms(h) * weight.  x, residual, h and y are
+    matrices of one type and size with neighbouring columns; weight and rstd
+    fp32 vectors; operand and operand_t device buffers of
+    demo_block_layout(rows, cols) and demo_block_layout(cols, rows) bytes."""
+    dev = _here(x, "x")
+    addr, ld = _matrix(x, "x", dev)
+    rows, cols = x.shape
+    res, ld_res = _maybe_matrix(residual, "residual", dev, x)
+    to_h, ld_h = _maybe_matrix(h, "h", dev, x)
+    to_y, ld_y = _maybe_matrix(y, "y", dev, x)
+    c = cfg.c(_dtype(x, "x")) if isinstance(cfg, Norm) else cfg
+    _check(lib().demo_rms_norm(ctypes.byref(c), rows, cols, addr, ld, res, ld_res, _vector(weight, "weight", dev, cols),
+                               to_h, ld_h, to_y, ld_y, _vector(rstd, "rstd", dev, rows),
+                               _operand_buf(operand, "operand", rows, cols, dev),
+                               _operand_buf(operand_t, "operand_t", cols, rows, dev), _stream(stream, dev)),
+           "demo_rms_norm")
+
+
+def demo_rms_norm_workspace(cfg, rows: int, cols: int) -> int:
+    """Bytes of workspace of demo_rms_norm_backward where dweight is wanted."""
+    out = ctypes.c_uint64()
+    c = cfg.c() if isinstance(cfg, Norm) else cfg
+    _check(lib().demo_rms_norm_workspace(ctypes.byref(c), rows, cols, ctypes.byref(out)), "demo_rms_norm_workspace")
+    return int(out.value)
+
+
+def demo_rms_norm_backward(cfg, dy, h, weight, rstd, dx, dresidual=None, dweight=None, addend=None, workspace=None,
+                           stream=None) -> None:
+    """dx and dweight = addend + ... of demo_rms_norm, from its h and rstd (h is
+    x where there was no residual).  dy, h, dresidual and dx are matrices of one
+    type and size with neighbouring columns, the rest fp32 vectors."""
+    dev = _here(dy, "dy")
+    addr, ld = _matrix(dy, "dy", dev)
+    rows, cols = dy.shape
+    at_h, ld_h = _matrix(h, "h", dev, (rows, cols), dy.dtype)
+    res, ld_res = _maybe_matrix(dresidual, "dresidual", dev, dy)
+    to, ld_dx = _matrix(dx, "dx", dev, (rows, cols), dy.dtype)
+    c = cfg.c(_dtype(dy, "dy")) if isinstance(cfg, Norm) else cfg
+    work, have = _workspace(workspace, dev)
+    _check(lib().demo_rms_norm_backward(ctypes.byref(c), rows, cols, addr, ld, at_h, ld_h,
+                                        _vector(weight, "weight", dev, cols), _vector(rstd, "rstd", dev, rows), res,
+                                        ld_res, to, ld_dx, _vector(dweight, "dweight", dev, cols),
+                                        _vector(addend, "addend", dev, cols), work, have, _stream(stream, dev)),
+           "demo_rms_norm_backward")
+
+
+class Tensors:
+    """A list of gradients for demo_grad_norm and demo_grad_clip: contiguous
+    device tensors of one device, held here with the table that the library
+    reads.  A program makes it once for tensors that stay where they are."""
+
+    def __init__(self, tensors):
+        self.tensors = list(tensors)
+        self.device = None
+        if len(self.tensors) > MAX_TENSORS:
+            raise ValueError(f"tensors: {len(self.tensors)} of them, at most {MAX_TENSORS}")
+        self.table = (demo_tensor * max(len(self.tensors), 1))()
+        for i, t in enumerate(self.tensors):
+            what = f"tensors[{i}]"
+            if not t.is_cuda:
+                raise ValueError(f"{what}: expected a device tensor")
+            if self.device is None:
+                self.device = t.get_device()
+            if t.get_device() != self.device:
+                raise ValueError(f"{what}: on device {t.get_device()}, tensors[0] on {self.device}")
+            if not t.is_contiguous():
+                raise ValueError(f"{what}: expected a contiguous tensor")
+            self.table[i] = demo_tensor(t.data_ptr() or None, t.numel(), _dtype(t, what), 0)
+
+    def __len__(self) -> int:
+        return len(self.tensors)
+
+    def check(self, what: str, dev: int) -> None:
+        if self.device not in (None, dev):
+            raise ValueError(f"{what}: on device {self.device}, not the current one")
+
+
+def _tensors(t, what: str, dev: int) -> Tensors:
+    t = t if isinstance(t, Tensors) else Tensors(t)
+    t.check(what, dev)
+    return t
+
+
+def _scalar(t, what: str, dev: int, dtype: str) -> int | None:
+    """Address of a device tensor whose first element a call reads or writes."""
+    if t is None:
+        return None
+    if t.get_device() != dev:
+        _here(t, what)
+    if str(t.dtype) != dtype:
+        raise TypeError(f"{what}: expected {dtype}, got {t.dtype}")
+    return _buf(t, what, t.element_size())
+
+
+def demo_grad_workspace(tensors) -> int:
+    """Bytes of workspace of demo_grad_norm for a list of tensors."""
+    out = ctypes.c_uint64()
+    t = tensors if isinstance(tensors, Tensors) else Tensors(tensors)
+    _check(lib().demo_grad_workspace(len(t), t.table, ctypes.byref(out)), "demo_grad_workspace")
+    return int(out.value)
+
+
+def demo_grad_norm(tensors, sumsq, workspace=None, stream=None) -> None:
+    """sumsq[0] = sum of the squares of all elements: tensors is a Tensors or a
+    list of tensors, sumsq a float64 device tensor."""
+    dev = _here(sumsq, "sumsq")
+    t = _tensors(tensors, "tensors", dev)
+    work, have = _workspace(workspace, dev)
+    _check(lib().demo_grad_norm(len(t), t.table, _scalar(sumsq, "sumsq", dev, "torch.float64"), work, have,
+                                _stream(stream, dev)), "demo_grad_norm")
+
+
+def demo_grad_clip(src, sumsq, max_norm: float, dst=None, norm=None, stream=None) -> None:
+    """dst[i] = min(1, max_norm / (sqrt(sumsq[0]) + 1e-6)) * src[i] for two lists
+    (Tensors or lists) of tensors; dst None: in place.  norm[0] (float32) =
+    sqrt(sumsq[0])."""
+    dev = _here(sumsq, "sumsq")
+    s = _tensors(src, "src", dev)
+    d = None if dst is None else _tensors(dst, "dst", dev)
+    if d is not None and len(d) != len(s):
+        raise ValueError(f"dst: {len(d)} tensors, src has {len(s)}")
+    _check(lib().demo_grad_clip(len(s), s.table, None if d is None else d.table,
+                                _scalar(sumsq, "sumsq", dev, "torch.float64"), max_norm,
+                                _scalar(norm, "norm", dev, "torch.float32"), _stream(stream, dev)), "demo_grad_clip")
+
+
+def demo_mx_layout(rows: int, cols: int) -> dict:
+    out = demo_operand()
+    _check(lib().demo_mx_layout(rows, cols, ctypes.byref(out)), "demo_mx_layout")
+    return out.as_dict()
+
+
+@functools.lru_cache(maxsize=1024)
+def _mx_bytes(rows: int, cols: int) -> int:
+    return demo_mx_layout(rows, cols)["total_bytes"]
+
+
+def _mx_buf(t, what: str, rows: int, cols: int, dev: int) -> int | None:
+    if t is None:
+        return None
+    if t.get_device() != dev:
+        _here(t, what)
+    return _buf(t, what, _mx_bytes(rows, cols))
+
+
+def demo_mx_quantize(cfg, src, operand=None, operand_t=None, dropout=None, stream=None) -> None:
+    """src: a matrix with neighbouring columns (rows may have a pitch);
+    operand and operand_t: device buffers of demo_mx_layout(rows, cols) and
+    demo_mx_layout(cols, rows) bytes."""
+    dev = _here(src, "src")
+    addr, ld = _matrix(src, "src", dev)
+    rows, cols = src.shape
+    c = cfg.c(_dtype(src, "src")) if isinstance(cfg, Mx) else cfg
+    _check(lib().demo_mx_quantize(ctypes.byref(c), rows, cols, addr, ld, _ref(dropout),
+                                  _mx_buf(operand, "operand", rows, cols, dev),
+                                  _mx_buf(operand_t, "operand_t", cols, rows, dev), _stream(stream, dev)),
+           "demo_mx_quantize")
+
+
+def demo_mx_dequantize(operand, dst, stream=None) -> None:
+    """dst (a matrix with neighbouring columns) = the values of the operand of
+    its size."""
+    dev = _here(dst, "dst")
+    addr, ld = _matrix(dst, "dst", dev)
+    rows, cols = dst.shape
+    c = demo_mx_cfg(ABI_VERSION, 0, _dtype(dst, "dst"), 0)
+    _check(lib().demo_mx_dequantize(ctypes.byref(c), rows, cols, _mx_buf(operand, "operand", rows, cols, dev), addr, ld,
+                                    _stream(stream, dev)), "demo_mx_dequantize")
+
+
+def demo_mx_workspace(cfg, m: int, n: int, k: int, dtype: int = DTYPE_F32) -> int:
+    """Bytes of workspace of a product whose result has the type dtype."""
+    out = ctypes.c_uint64()
+    c = cfg.c(dtype) if isinstance(cfg, Mx) else cfg
+    _check(lib().demo_mx_workspace(ctypes.byref(c), m, n, k, ctypes.byref(out)), "demo_mx_workspace")
+    return int(out.value)
+
+
+def demo_mx_matmul(cfg, m: int, n: int, k: int, a, b, c, addend=None, dropout=None, workspace=None,
+                   stream=None) -> None:
+    """c = addend + dropout(a b^T) for 4-bit operands a (m x k) and b (n x k); c
+    and addend are m x n matrices of one type with neighbouring columns."""
+    dev = _here(c, "c")
+    addr, ldc = _matrix(c, "c", dev, (m, n))
+    add, lda = _maybe_matrix(addend, "addend", dev, c)
+    cc = cfg.c(_dtype(c, "c")) if isinstance(cfg, Mx) else cfg
+    work, have = _workspace(workspace, dev)
+    _check(lib().demo_mx_matmul(ctypes.byref(cc), m, n, k, _mx_buf(a, "a", m, k, dev), _mx_buf(b, "b", n, k, dev),
+                                addr, ldc, add, lda, _ref(dropout), work, have, _stream(stream, dev)),
+           "demo_mx_matmul")
+
+
 # raw return codes (tests of the boundary's validation)
 def raw_encode(cfg, n_elems, grad, momentum, payload_out, q_out=None, stream=0) -> int:
     c = _cfg(cfg)
@@ -586,3 +863,71 @@ def raw_block_matmul(cfg, m, n, k, a, b, c, ldc, addend=None, ld_addend=0, dropo
                      workspace_bytes=0, stream=0) -> int:
     return int(lib().demo_block_matmul(None if cfg is None else ctypes.byref(cfg), m, n, k, a, b, c, ldc, addend,
                                        ld_addend, _ref(dropout), workspace, workspace_bytes, stream))
+
+
+def _byref(c):
+    return None if c is None else ctypes.byref(c)
+
+
+def raw_rms_norm(cfg, rows, cols, x, ld_x, residual, ld_residual, weight, h=None, ld_h=0, y=None, ld_y=0, rstd=None,
+                 operand=None, operand_t=None, stream=0) -> int:
+    return int(lib().demo_rms_norm(_byref(cfg), rows, cols, x, ld_x, residual, ld_residual, weight, h, ld_h, y, ld_y,
+                                   rstd, operand, operand_t, stream))
+
+
+def raw_rms_norm_workspace(cfg, rows, cols) -> tuple[int, int]:
+    out = ctypes.c_uint64()
+    rc = int(lib().demo_rms_norm_workspace(_byref(cfg), rows, cols, ctypes.byref(out)))
+    return rc, int(out.value)
+
+
+def raw_rms_norm_backward(cfg, rows, cols, dy, ld_dy, h, ld_h, weight, rstd, dresidual, ld_dresidual, dx, ld_dx,
+                          dweight=None, addend=None, workspace=None, workspace_bytes=0, stream=0) -> int:
+    return int(lib().demo_rms_norm_backward(_byref(cfg), rows, cols, dy, ld_dy, h, ld_h, weight, rstd, dresidual,
+                                            ld_dresidual, dx, ld_dx, dweight, addend, workspace, workspace_bytes,
+                                            stream))
+
+
+def raw_tensors(*entries):
+    """A table of (address, elements, type[, reserved]) entries."""
+    return (demo_tensor * max(len(entries), 1))(*(demo_tensor(*(e if len(e) == 4 else (*e, 0))) for e in entries))
+
+
+def raw_grad_workspace(count, tensors) -> tuple[int, int]:
+    out = ctypes.c_uint64()
+    rc = int(lib().demo_grad_workspace(count, tensors, ctypes.byref(out)))
+    return rc, int(out.value)
+
+
+def raw_grad_norm(count, tensors, sumsq, workspace=None, workspace_bytes=0, stream=0) -> int:
+    return int(lib().demo_grad_norm(count, tensors, sumsq, workspace, workspace_bytes, stream))
+
+
+def raw_grad_clip(count, src, dst, sumsq, max_norm, norm=None, stream=0) -> int:
+    return int(lib().demo_grad_clip(count, src, dst, sumsq, max_norm, norm, stream))
+
+
+def raw_mx_layout(rows, cols) -> tuple[int, dict]:
+    out = demo_operand()
+    rc = int(lib().demo_mx_layout(rows, cols, ctypes.byref(out)))
+    return rc, out.as_dict()
+
+
+def raw_mx_quantize(cfg, rows, cols, src, ld, dropout, operand, operand_t, stream=0) -> int:
+    return int(lib().demo_mx_quantize(_byref(cfg), rows, cols, src, ld, _ref(dropout), operand, operand_t, stream))
+
+
+def raw_mx_dequantize(cfg, rows, cols, operand, dst, ld, stream=0) -> int:
+    return int(lib().demo_mx_dequantize(_byref(cfg), rows, cols, operand, dst, ld, stream))
+
+
+def raw_mx_workspace(cfg, m, n, k) -> tuple[int, int]:
+    out = ctypes.c_uint64()
+    rc = int(lib().demo_mx_workspace(_byref(cfg), m, n, k, ctypes.byref(out)))
+    return rc, int(out.value)
+
+
+def raw_mx_matmul(cfg, m, n, k, a, b, c, ldc, addend=None, ld_addend=0, dropout=None, workspace=None,
+                  workspace_bytes=0, stream=0) -> int:
+    return int(lib().demo_mx_matmul(_byref(cfg), m, n, k, a, b, c, ldc, addend, ld_addend, _ref(dropout), workspace,
+                                    workspace_bytes, stream))

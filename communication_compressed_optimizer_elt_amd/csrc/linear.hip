@@ -7,61 +7,23 @@
 #include <cstring>
 
 #include "demo.h"
-#include "host.hpp"
+#include "linear_host.hpp"
 #include "product_big.hpp"
 #include "quantize.hpp"
 
 namespace {
 
 using demo::aligned16;
+using demo::aligned_to;
+using demo::drop_of;
+using demo::elem_bytes;
 using demo::launch;
+using demo::operand_of;
 using demo::overlap;
+using demo::pitch_ok;
+using demo::sides_ok;
 using demo::status_of;
-
-constexpr uint64_t kMaxSide = (uint64_t)1 << 30;  // grids stay below 2^32 work-items, indices below 2^32
-
-uint64_t up(uint64_t x, uint64_t a) { return (x + a - 1) / a * a; }
-
-uint64_t elem_bytes(uint32_t dtype) { return dtype == DEMO_DTYPE_F32 ? 4 : 2; }
-
-bool aligned_to(const void* p, uint64_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
-
-bool sides_ok(uint64_t rows, uint64_t cols) {
-    return rows >= 1 && cols >= 1 && rows <= kMaxSide && cols <= kMaxSide && rows * cols <= DEMO_MAX_ELEMS;
-}
-
-// a row pitch that keeps every index of the matrix in 64 bits with room to spare
-bool pitch_ok(uint64_t rows, uint64_t cols, uint64_t ld) {
-    return ld >= cols && ld <= DEMO_MAX_ELEMS && rows - 1 <= ((uint64_t)1 << 40) / ld;
-}
-
-demo_operand operand_of(uint64_t rows, uint64_t cols) {
-    demo_operand o{};
-    o.pitch = up(cols, DEMO_BLOCK);
-    o.scale_pitch = up(o.pitch / DEMO_BLOCK, 4);
-    o.scale_off = demo::up256(rows * o.pitch);
-    o.total_bytes = demo::up256(o.scale_off + rows * o.scale_pitch);
-    return o;
-}
-
-// demo::Drop of a configuration for n elements, or an error code
-int drop_of(const demo_dropout_cfg* cfg, uint64_t n, demo::Drop* d) {
-    *d = demo::Drop{};
-    if (!cfg) return DEMO_OK;
-    if (cfg->abi_version != DEMO_ABI_VERSION) return DEMO_EABI;
-    if (!(cfg->p >= 0.f && cfg->p <= 1.f) || cfg->site >= (1u << 24) || cfg->reserved != 0) return DEMO_EINVAL;
-    const uint64_t last = (uint64_t)1 << 59;  // the element's number fits 64 bits
-    if (cfg->chunk_offset > last || cfg->chunk_offset + (n + 31) / 32 > last) return DEMO_EINVAL;
-    d->first = cfg->chunk_offset * (DEMO_CHUNK / 8);
-    d->k0 = (uint32_t)cfg->seed;
-    d->k1 = (uint32_t)(cfg->seed >> 32);
-    d->step = (uint32_t)cfg->step;
-    d->c3 = (demo::kTagDropout << 24) | cfg->site;
-    d->threshold = (uint32_t)std::floor((double)cfg->p * 65536.0 + 0.5);
-    d->scale = d->threshold == 65536u ? 0.f : (float)(65536.0 / (65536.0 - (double)d->threshold));
-    d->on = 1;
-    return DEMO_OK;
-}
+using demo::up;
 
 template <typename T>
 hipError_t launch_dropout(const demo::DropoutArgs& a, hipStream_t s) {
@@ -212,7 +174,7 @@ hipError_t launch_product(demo::ProductArgs a, const Plan& plan, void* workspace
     else e = launch(demo::product_big_kernel<FA, FB>, grid, dim3(256), demo::kBigLds, s, a);
     if (e != hipSuccess || plan.splits == 1) return e;
     const uint64_t blocks = ((uint64_t)a.m * ((a.n + 7) / 8) + 255) / 256;
-    return launch(demo::product_join_kernel, dim3((unsigned)(blocks < (1u << 20) ? blocks : (1u << 20))), dim3(256), 0, s,
+    return launch(demo::product_join_kernel<>, dim3((unsigned)(blocks < (1u << 20) ? blocks : (1u << 20))), dim3(256), 0, s,
                   a, plan.splits);
 }
 

@@ -620,6 +620,7 @@ __global__ __launch_bounds__(256) void product_rows_kernel(ProductArgs p) {
 // The splits' partial sums, added in their order, to the result.  They were
 // written just before and come from the caches; what this costs is in the
 // figures by which sums are split.
+template <typename = void>
 __global__ __launch_bounds__(256) void product_join_kernel(ProductArgs p, uint32_t splits) {
     const uint32_t groups = (p.n + 7) / 8;
     const uint64_t total = (uint64_t)p.m * groups, plane = (uint64_t)p.m * p.n;

@@ -368,6 +368,162 @@ int demo_block_matmul(const demo_product_cfg *cfg, uint64_t m, uint64_t n, uint6
                       void *c, uint64_t ldc, const void *addend, uint64_t ld_addend,
                       const demo_dropout_cfg *dropout, void *workspace, uint64_t workspace_bytes, void *hip_stream);
 
+/*
+ * Root-mean-square norm in front of a linear layer, with the residual's
+ * addition before it and the layer's 8-bit operand behind it:
+ *   h = residual + x            in fp32, rounded to the tensors' type dtype,
+ *   r = 1 / sqrt(mean over the row of h^2 + eps),
+ *   y = (h * r) * weight        in fp32.
+ */
+#define DEMO_NORM_MAX_COLS 16384
+
+typedef struct demo_norm_cfg {
+    uint32_t abi_version; /* must be DEMO_ABI_VERSION */
+    uint32_t dtype;       /* DEMO_DTYPE_* of x, residual, h and y, or of the gradients */
+    uint32_t fmt;         /* DEMO_FMT_* of the operands' codes */
+    float eps;            /* finite, at least 0 */
+} demo_norm_cfg;
+
+/*
+ * x, residual, h, y: [rows][cols] with row pitches in elements, aligned to
+ * their element ((rows - 1) * pitch at most 2^40); weight fp32 [cols], rstd
+ * fp32 [rows], 4-byte aligned.  Each output may be NULL, not all of them:
+ * h, y (rounded to dtype), rstd (r, which the backward pass reads), operand
+ * (y as demo_block_quantize quantises an fp32 y: rows x cols, blocks along the
+ * columns) and operand_t (cols x rows, blocks along the rows).  residual may be
+ * NULL (h = x).  operand_t is made from h and r, so it needs rstd, and h where
+ * there is a residual.  h and y may each be x or residual, in the same place
+ * with the same pitch (y not x where operand_t is made from x); otherwise what
+ * is written meets no other buffer of the call.  A row whose sum of squares
+ * passes fp32's range has r = 0; with eps = 0 a row of zeros gives NaN.  1 <=
+ * cols <= DEMO_NORM_MAX_COLS (DEMO_EUNSUPPORTED beyond), rows at most 2^30, rows
+ * * cols at most DEMO_MAX_ELEMS.
+ */
+int demo_rms_norm(const demo_norm_cfg *cfg, uint64_t rows, uint64_t cols, const void *x, uint64_t ld_x,
+                  const void *residual, uint64_t ld_residual, const float *weight, void *h, uint64_t ld_h, void *y,
+                  uint64_t ld_y, float *rstd, void *operand, void *operand_t, void *hip_stream);
+
+/* Bytes of workspace demo_rms_norm_backward needs for these sizes where
+ * dweight is wanted (at most DEMO_BLOCK_MAX_WORKSPACE); host-only. */
+int demo_rms_norm_workspace(const demo_norm_cfg *cfg, uint64_t rows, uint64_t cols, uint64_t *bytes);
+
+/*
+ * The gradients, from dy (of y), the forward pass' h and rstd, and dresidual
+ * (what reaches h from the residual's side; NULL: nothing): with n = h*r and g =
+ * dy*weight
+ *   dx      = r * (g - n * mean over the row of g*n) + dresidual,
+ *   dweight = addend + sum over the rows of dy*n,
+ * dx being the gradient of x and of residual alike.  Sums in fp32, in an order
+ * that the sizes fix; dx is rounded once to dtype.  dweight fp32 [cols] (NULL:
+ * not wanted, and no workspace is needed); addend fp32 [cols], NULL or dweight
+ * itself (to add to a gradient) among others.  dx may be dy, h or dresidual, in
+ * the same place with the same pitch.  cfg->fmt and cfg->eps are not used.  The
+ * workspace is one call's at a time, as demo_block_matmul's.
+ */
+int demo_rms_norm_backward(const demo_norm_cfg *cfg, uint64_t rows, uint64_t cols, const void *dy, uint64_t ld_dy,
+                           const void *h, uint64_t ld_h, const float *weight, const float *rstd,
+                           const void *dresidual, uint64_t ld_dresidual, void *dx, uint64_t ld_dx, float *dweight,
+                           const float *addend, void *workspace, uint64_t workspace_bytes, void *hip_stream);
+
+/*
+ * Between the backward pass and demo_encode: the norm of the whole gradient,
+ * and its clipped copy.  The gradient is a list of tensors, each contiguous,
+ * of one of the types, aligned to its element, possibly empty (data may then be
+ * NULL).  The list is host memory, read when the call is made.
+ */
+#define DEMO_MAX_TENSORS 65536
+
+typedef struct demo_tensor {
+    void *data;
+    uint64_t n_elems;  /* at most DEMO_MAX_ELEMS */
+    uint32_t dtype;    /* DEMO_DTYPE_* */
+    uint32_t reserved; /* must be 0 */
+} demo_tensor;
+
+/* Bytes of workspace demo_grad_norm needs for this list (0 for small ones, at
+ * most DEMO_BLOCK_MAX_WORKSPACE); host-only. */
+int demo_grad_workspace(uint32_t count, const demo_tensor *tensors, uint64_t *bytes);
+
+/*
+ * *sumsq = sum of the squares of all elements, in fp64 in an order that the
+ * list fixes (a tensor that stands in it twice counts twice; 0 for nothing).
+ * sumsq: device double, 8-byte aligned.  Where the gradient is spread over
+ * shards, add the shards' sums up before demo_grad_clip.
+ */
+int demo_grad_norm(uint32_t count, const demo_tensor *tensors, double *sumsq, void *workspace,
+                   uint64_t workspace_bytes, void *hip_stream);
+
+/*
+ * dst = c * src tensor by tensor, in fp32 and rounded once, with
+ *   c = min(1, max_norm / (sqrt(*sumsq) + 1e-6)),
+ * and *norm = sqrt(*sumsq) (device float; NULL: not wanted).  dst holds as many
+ * tensors of the same sizes, each of src's type or fp32: pieces of the flat fp32
+ * gradient that demo_encode reads, for instance.  dst NULL: in place, and then
+ * a gradient within max_norm is neither read nor written.  A tensor of dst may
+ * be the same one of src (type too); otherwise what is written meets nothing
+ * else.  max_norm >= 0, infinity included.  Infinities in the gradient make c 0
+ * (and 0 * infinity is NaN), a NaN makes all of it NaN: a caller that skips such
+ * steps reads *norm.
+ */
+int demo_grad_clip(uint32_t count, const demo_tensor *src, const demo_tensor *dst, const double *sumsq,
+                   float max_norm, float *norm, void *hip_stream);
+
+/*
+ * The same linear layer on 4-bit operands: e2m1 codes (OCP microscaling; 0, 0.5,
+ * 1, 1.5, 2, 3, 4, 6 and their negatives) with a power of two for each block of
+ * 32 along the sum.
+ */
+#define DEMO_MX_BLOCK 32
+
+typedef struct demo_mx_cfg {
+    uint32_t abi_version; /* must be DEMO_ABI_VERSION */
+    uint32_t tile;  /* quantiser: 0: a scale for 32 values of a row; 1: for a square of 32 x 32; else 0 */
+    uint32_t dtype; /* DEMO_DTYPE_* of src, dst, or c and addend */
+    uint32_t reserved; /* must be 0 */
+} demo_mx_cfg;
+
+/*
+ * Layout of a 4-bit operand of rows x cols (cols is the summed axis);
+ * host-only: rows of codes with a pitch of the next multiple of 256 codes, two
+ * in a byte, the even column in the low half (codes behind the last column are
+ * 0), then at scale_off one byte e + 127 for each row and block of 32 columns,
+ * with a pitch of the next multiple of 16 bytes.  A code c of that block stands
+ * for c * 2^e, whatever the code for NaN where the byte is 255.  Operands are
+ * 16-byte aligned.  Sizes as for demo_block_layout.
+ */
+int demo_mx_layout(uint64_t rows, uint64_t cols, demo_operand *out);
+
+/*
+ * demo_block_quantize to 4-bit operands: src [rows][cols] into operand and its
+ * transposed matrix into operand_t, in one pass; one of the two may be NULL.
+ * A block's scale is 2^e with the smallest e >= -127 that keeps its largest
+ * magnitude within 6 * 2^e; codes are rounded to nearest even.  The format has
+ * neither infinity nor NaN: a block with one of them has the scale byte 255 and
+ * stands for NaN as a whole.  With dropout the values are first multiplied as
+ * demo_dropout_backward does, in fp32 without a rounding between.
+ */
+int demo_mx_quantize(const demo_mx_cfg *cfg, uint64_t rows, uint64_t cols, const void *src, uint64_t ld,
+                     const demo_dropout_cfg *dropout, void *operand, void *operand_t, void *hip_stream);
+
+/* The values that an operand stands for, rounded once to dst's type: dst
+ * [rows][cols], row pitch ld elements, aligned to its element. */
+int demo_mx_dequantize(const demo_mx_cfg *cfg, uint64_t rows, uint64_t cols, const void *operand, void *dst,
+                       uint64_t ld, void *hip_stream);
+
+/* Bytes of workspace demo_mx_matmul needs for these sizes (0 for most, at most
+ * DEMO_BLOCK_MAX_WORKSPACE); host-only. */
+int demo_mx_workspace(const demo_mx_cfg *cfg, uint64_t m, uint64_t n, uint64_t k, uint64_t *bytes);
+
+/*
+ * demo_block_matmul on 4-bit operands a (m x k) and b (n x k):
+ *   c[i][j] = addend[i][j] + drop(sum over k of a[i][k]*b[j][k]),
+ * with its rules for addend, dropout, pitches, overlaps, sizes and workspace.
+ * Products are exact and sums are held in fp32 for every type of the result.
+ */
+int demo_mx_matmul(const demo_mx_cfg *cfg, uint64_t m, uint64_t n, uint64_t k, const void *a, const void *b, void *c,
+                   uint64_t ldc, const void *addend, uint64_t ld_addend, const demo_dropout_cfg *dropout,
+                   void *workspace, uint64_t workspace_bytes, void *hip_stream);
+
 #ifdef __cplusplus
 }
 #endif
