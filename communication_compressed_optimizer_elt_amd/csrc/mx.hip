@@ -69,6 +69,12 @@ hipError_t launch_quantize(const demo::MxArgs& a, bool wide, dim3 grid, hipStrea
 // the kernel for few rows, and the columns that its grid holds (below 2^32 work-items)
 constexpr uint64_t kFewRows = 16, kFewRowsMaxCols = (uint64_t)1 << 26;
 
+constexpr uint32_t kCus = 256;
+
+// Results up to this many bytes stay in the caches for who reads them next,
+// larger ones go past them.
+constexpr uint64_t kCached = (uint64_t)96 << 20;
+
 // How a product is cut: tiles of `tile` x `tile` and `splits` of the sum, or
 // (tile 0) the kernel for few rows.
 struct Plan {
@@ -81,6 +87,9 @@ Plan plan_of(uint64_t m, uint64_t n, uint64_t k) {
     const uint64_t kb = up(k, kStep) / kStep;
     if (m <= kFewRows && n <= kFewRowsMaxCols) return {0, 1, (uint32_t)kb};
     const auto tiles = [&](uint64_t t) { return up(m, t) / t * (up(n, t) / t); };
+    const auto rounds = [](uint64_t count, uint64_t at_once) { return (count + at_once - 1) / at_once; };
+    if (m >= 256 && n >= 256 && 33 * rounds(tiles(256), 256) <= 20 * rounds(tiles(128), 512))
+        return {256, 1, (uint32_t)up(kb, 2)};
     const uint64_t tile = tiles(128) > 256u ? 128 : 64, least = tile == 128 ? 32 : 8;
     uint64_t splits = 512 / tiles(tile);
     if (splits > kb / least) splits = kb / least;
@@ -97,6 +106,24 @@ hipError_t launch_tiles(const demo::ProductArgs& a, dim3 grid, hipStream_t s) {
     return launch(demo::mx_kernel<TILE, TILE, 2, 2>, grid, dim3(256), lds, s, a);
 }
 
+template <typename T>
+hipError_t launch_stream(const demo::ProductArgs& a, hipStream_t s) {
+    const uint32_t tiles = a.tiles_m * a.tiles_n;
+    const bool past = (uint64_t)a.m * a.n * sizeof(T) > kCached;
+    return launch(past ? demo::mx_stream_kernel<T, true> : demo::mx_stream_kernel<T, false>,
+                  dim3(tiles < kCus ? tiles : kCus), dim3(256), demo::kMxStreamLds, s, a);
+}
+
+// 256 x 256 tiles: by workgroups that stay where nothing but the sums goes to C
+hipError_t launch_big(const demo::ProductArgs& a, hipStream_t s) {
+    const bool plain = a.wide && !a.addend && !a.drop.on && a.kb % 2 == 0 && a.kb >= 4 && a.ldc < ((uint64_t)1 << 25);
+    if (plain) {
+        if (a.dtype == DEMO_DTYPE_F32) return launch_stream<float>(a, s);
+        return a.dtype == DEMO_DTYPE_F16 ? launch_stream<demo::f16_t>(a, s) : launch_stream<demo::bf16_t>(a, s);
+    }
+    return launch(demo::mx_big_kernel<>, dim3(a.tiles_m * a.tiles_n), dim3(256), demo::kMxBigLds, s, a);
+}
+
 hipError_t launch_product(demo::ProductArgs a, const Plan& plan, void* workspace, hipStream_t s) {
     if (plan.tile == 0) return launch(demo::mx_few_kernel<8>, dim3((a.n + 15) / 16), dim3(512), 0, s, a);
     a.kb_split = plan.kb_split;
@@ -104,7 +131,9 @@ hipError_t launch_product(demo::ProductArgs a, const Plan& plan, void* workspace
     a.tiles_m = (a.m + plan.tile - 1) / plan.tile;
     a.tiles_n = (a.n + plan.tile - 1) / plan.tile;
     const dim3 grid(a.tiles_m * a.tiles_n, plan.splits);
-    const hipError_t e = plan.tile == 64 ? launch_tiles<64>(a, grid, s) : launch_tiles<128>(a, grid, s);
+    const hipError_t e = plan.tile == 64    ? launch_tiles<64>(a, grid, s)
+                         : plan.tile == 128 ? launch_tiles<128>(a, grid, s)
+                                            : launch_big(a, s);
     if (e != hipSuccess || plan.splits == 1) return e;
     const uint64_t blocks = ((uint64_t)a.m * ((a.n + 7) / 8) + 255) / 256;
     return launch(demo::product_join_kernel<>, dim3((unsigned)(blocks < (1u << 20) ? blocks : (1u << 20))), dim3(256), 0, s,

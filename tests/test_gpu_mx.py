@@ -234,6 +234,38 @@ def test_product(torch, m, n, k, dtype):
     check_product(torch, acc, a, b, add)
 
 
+@pytest.mark.parametrize("k", [100, 257, 520, 1024, 1100, 1500, 2000])
+@pytest.mark.parametrize("m,n", [(4100, 2060), (2100, 4104)])
+def test_large_product(torch, m, n, k):
+    """Tiles of 256 with every number of steps up to 8, moved back inside at both ends."""
+    (qa, a), (qb, b) = packed(torch, k, m, k), packed(torch, n, n, k)
+    c = torch.full((m, n), 9.0, dtype=torch.bfloat16, device="cuda")
+    add = normal(torch, 3, m, n, std=10.0)
+    acc = add.clone()
+    L.demo_mx_matmul(L.Mx(), m, n, k, qa, qb, c)
+    L.demo_mx_matmul(L.Mx(), m, n, k, qa, qb, acc, addend=acc)
+    check_product(torch, c, a, b)
+    check_product(torch, acc, a, b, add)
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("k", [1024, 1500, 2048, 2300])
+def test_several_tiles_a_workgroup(torch, k, dtype):
+    """561 tiles of 256: up to three one after another, the last ones moved back inside."""
+    m, n = 8200, 4104
+    (qa, a), (qb, b) = packed(torch, k, m, k), packed(torch, n, n, k)
+    c = torch.full((m + 1, n), 9.0, dtype=getattr(torch, dtype), device="cuda")
+    L.demo_mx_matmul(L.Mx(), m, n, k, qa, qb, c[:m])
+    assert (c[m] == 9.0).all()
+    a, b = torch.from_numpy(a).cuda(), torch.from_numpy(b).cuda()
+    want, s = a @ b.t(), a.abs() @ b.abs().t()
+    f = torch.finfo(c.dtype)
+    err = (17 * -(-k // 128) + 64) * 2.0**-23 * s + 2.0**-23 * want.abs()
+    bound = err + f.eps / 2 * (want.abs() + err) + f.tiny * f.eps / 2
+    over = (want.abs() + err >= f.max) & c[:m].isinf() & (c[:m] * want > 0)  # as in check_product
+    assert (over | ((c[:m].double() - want).abs() <= bound)).all()
+
+
 @pytest.mark.parametrize("dtype", DT)
 @pytest.mark.parametrize("m,n,k", [(1, 70, 300), (2, 70, 300), (12, 70, 300), (140, 133, 300), (300, 270, 600), (64, 64, 16384)])
 def test_product_slices(torch, dtype, m, n, k):
