@@ -57,45 +57,62 @@ struct Shape {
     static constexpr int kWaves = W, kVectors = NV;
 };
 
-// A row of up to 2048 columns is a wave's, which then needs no barrier, unless
-// there are too few rows to fill the card with such waves; a longer one is four
-// waves', or sixteen's.
+// Waves that share a row: 512 columns each, and twice that for the longest rows.
 template <typename F>
-hipError_t with_shape(uint64_t rows, uint64_t cols, F f) {
-    if (cols <= 512) return f(Shape<1, 1>());
-    if (cols <= 2048 && rows <= 2048) return f(Shape<4, 1>());
-    if (cols <= 1024) return f(Shape<1, 2>());
-    if (cols <= 2048) return f(Shape<1, 4>());
-    if (cols <= 4096) return f(Shape<4, 2>());
-    if (cols <= 8192) return f(Shape<4, 4>());
-    return f(Shape<16, 2>());
+hipError_t with_shape(uint64_t cols, F f) {
+    switch ((cols + 511) / 512) {
+    case 1: return f(Shape<1, 1>());
+    case 2: return f(Shape<2, 1>());
+    case 3: return f(Shape<3, 1>());
+    case 4: return f(Shape<4, 1>());
+    case 5: return f(Shape<5, 1>());
+    case 6: return f(Shape<6, 1>());
+    case 7:
+    case 8: return f(Shape<8, 1>());
+    case 9:
+    case 10: return f(Shape<10, 1>());
+    case 11:
+    case 12: return f(Shape<12, 1>());
+    case 13:
+    case 14:
+    case 15:
+    case 16: return f(Shape<16, 1>());
+    default: return f(Shape<16, 2>());
+    }
 }
 static_assert(DEMO_NORM_MAX_COLS == 16 * 2 * 512, "the longest row");
 
-template <typename S>
-uint32_t grid_of(uint64_t rows, uint32_t most) {
-    const uint64_t each = S::kWaves < 4 ? 4 / S::kWaves : 1, blocks = (rows + each - 1) / each;
+uint32_t grid_of(uint64_t rows, uint64_t each, uint32_t most) {
+    const uint64_t blocks = (rows + each - 1) / each;
     return (uint32_t)(blocks < most ? blocks : most);
 }
 
-// the backward pass' workgroups, each with a sum for each column
+// The backward pass' workgroups, each with a sum for each column: two a CU, or
+// one where a row is more than eight waves' (16384 x 2048 bf16: 53.2 us, 56 to 61
+// with 384, 640 or 768 of them; 4096 x 8192: 57.4 us, 64 with 512).
+constexpr uint32_t kBackGrid = 512;
+template <typename S>
+uint32_t back_grid(uint64_t rows) {
+    return grid_of(rows, demo::kBackRows<S::kWaves>, S::kWaves <= 8 ? kBackGrid : kBackGrid / 2);
+}
 uint32_t back_grid(uint64_t rows, uint64_t cols) {
     uint32_t grid = 0;
-    (void)with_shape(rows, cols, [&](auto shape) {
-        grid = grid_of<decltype(shape)>(rows, 1024);
+    (void)with_shape(cols, [&](auto shape) {
+        grid = back_grid<decltype(shape)>(rows);
         return hipSuccess;
     });
     return grid;
 }
-static_assert((uint64_t)1024 * DEMO_NORM_MAX_COLS * 4 <= DEMO_BLOCK_MAX_WORKSPACE, "workspace");
+static_assert((uint64_t)kBackGrid * DEMO_NORM_MAX_COLS * 4 <= DEMO_BLOCK_MAX_WORKSPACE, "workspace");
 
 template <typename T>
 hipError_t launch_norm(const demo::NormArgs& a, bool wide, hipStream_t s) {
-    return with_shape(a.rows, a.cols, [&](auto shape) {
+    return with_shape(a.cols, [&](auto shape) {
         typedef decltype(shape) S;
         constexpr int W = S::kWaves, NV = S::kVectors;
         return launch(wide ? demo::norm_kernel<T, W, NV, true> : demo::norm_kernel<T, W, NV, false>,
-                      dim3(grid_of<S>(a.rows, 2048)), dim3(W < 4 ? 256 : 64 * W), 0, s, a);
+                      dim3(grid_of(a.rows, demo::kNormWaves<W> / W, W <= 6 ? 1u << 20 : W <= 8 ? 4096 : 512)),
+                      dim3(64 * demo::kNormWaves<W>), 0, s, a);
     });
 }
 
@@ -111,11 +128,11 @@ hipError_t launch_turn(const demo::NormTurnArgs& a, uint32_t fmt, bool wide, hip
 
 template <typename T>
 hipError_t launch_back(const demo::NormBackArgs& a, bool wide, hipStream_t s) {
-    return with_shape(a.rows, a.cols, [&](auto shape) {
+    return with_shape(a.cols, [&](auto shape) {
         typedef decltype(shape) S;
         constexpr int W = S::kWaves, NV = S::kVectors;
         return launch(wide ? demo::norm_back_kernel<T, W, NV, true> : demo::norm_back_kernel<T, W, NV, false>,
-                      dim3(grid_of<S>(a.rows, 1024)), dim3(W < 4 ? 256 : 64 * W), 0, s, a);
+                      dim3(back_grid<S>(a.rows)), dim3(64 * W * demo::kBackRows<W>), 0, s, a);
     });
 }
 
@@ -196,8 +213,8 @@ int demo_rms_norm(const demo_norm_cfg* cfg, uint64_t rows, uint64_t cols, const 
         t.s_pitch_t = (uint32_t)ot.scale_pitch;
         t.rows = a.rows;
         t.cols = a.cols;
-        t.tiles_c = (uint32_t)(o.pitch / DEMO_BLOCK);
-        return launch_turn<T>(t, cfg->fmt, wide, s);
+        t.tiles_c = (a.cols + 63) / 64;
+        return launch_turn<T>(t, cfg->fmt, wide && aligned16(rstd), s);
     }));
 }
 
@@ -253,7 +270,7 @@ int demo_rms_norm_backward(const demo_norm_cfg* cfg, uint64_t rows, uint64_t col
     hipStream_t s = static_cast<hipStream_t>(hip_stream);
     const hipError_t e = with_type(cfg->dtype, [&](auto type) { return launch_back<decltype(type)>(a, wide, s); });
     if (e != hipSuccess || !need) return status_of(e);
-    return status_of(launch(demo::norm_join_kernel, dim3((a.cols + 31) / 32), dim3(1024), 0, s, a.partial,
+    return status_of(launch(demo::norm_join_kernel, dim3((a.cols + demo::kJoinCols - 1) / demo::kJoinCols), dim3(1024), 0, s, a.partial,
                             (uint32_t)grid, a.cols, addend, dweight));
 }
 

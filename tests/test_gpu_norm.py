@@ -14,7 +14,7 @@ with the quotient.
             a border.
   dx        n and g one product each; the mean 64 e A, A the mean of |g n|;
             r (4 |g| + |n| (66 A + 4 |mean|)) e + 3 (|dres| + |dx|) e + u |dx|.
-  dweight   a row's n and product, 8 rows in a lane, 3 waves, 32 + 32 workgroups: 80 e
+  dweight   n and product, 3 rows in a lane, 7 of a workgroup, 12 and 64 workgroups: 80 e
             sum |dy n| + e (|addend| + |dw|).
 """
 import linear_forms as F
