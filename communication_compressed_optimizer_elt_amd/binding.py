@@ -593,7 +593,9 @@ def _workspace(t, dev: int) -> tuple[int | None, int]:
         return None, 0
     if t.get_device() != dev:
         _here(t, "workspace")
-    return _buf(t, "workspace", 0), t.numel() * t.element_size()
+    if not t.is_contiguous():
+        raise ValueError("workspace: expected a contiguous tensor")
+    return t.data_ptr(), t.numel() * t.element_size()
 
 
 def demo_rms_norm(cfg, x, weight, y=None, residual=None, h=None, rstd=None, operand=None, operand_t=None,
@@ -681,15 +683,24 @@ def _tensors(t, what: str, dev: int) -> Tensors:
     return t
 
 
+@functools.lru_cache(maxsize=None)
+def _torch():
+    import torch
+
+    return torch
+
+
 def _scalar(t, what: str, dev: int, dtype: str) -> int | None:
     """Address of a device tensor whose first element a call reads or writes."""
     if t is None:
         return None
     if t.get_device() != dev:
         _here(t, what)
-    if str(t.dtype) != dtype:
+    if t.dtype != getattr(_torch(), dtype):
         raise TypeError(f"{what}: expected {dtype}, got {t.dtype}")
-    return _buf(t, what, t.element_size())
+    if t.numel() < 1:
+        raise ValueError(f"{what}: holds nothing, the call needs one element")
+    return t.data_ptr()
 
 
 def demo_grad_workspace(tensors) -> int:
@@ -706,7 +717,7 @@ def demo_grad_norm(tensors, sumsq, workspace=None, stream=None) -> None:
     dev = _here(sumsq, "sumsq")
     t = _tensors(tensors, "tensors", dev)
     work, have = _workspace(workspace, dev)
-    _check(lib().demo_grad_norm(len(t), t.table, _scalar(sumsq, "sumsq", dev, "torch.float64"), work, have,
+    _check(lib().demo_grad_norm(len(t), t.table, _scalar(sumsq, "sumsq", dev, "float64"), work, have,
                                 _stream(stream, dev)), "demo_grad_norm")
 
 
@@ -720,8 +731,8 @@ def demo_grad_clip(src, sumsq, max_norm: float, dst=None, norm=None, stream=None
     if d is not None and len(d) != len(s):
         raise ValueError(f"dst: {len(d)} tensors, src has {len(s)}")
     _check(lib().demo_grad_clip(len(s), s.table, None if d is None else d.table,
-                                _scalar(sumsq, "sumsq", dev, "torch.float64"), max_norm,
-                                _scalar(norm, "norm", dev, "torch.float32"), _stream(stream, dev)), "demo_grad_clip")
+                                _scalar(sumsq, "sumsq", dev, "float64"), max_norm,
+                                _scalar(norm, "norm", dev, "float32"), _stream(stream, dev)), "demo_grad_clip")
 
 
 def demo_mx_layout(rows: int, cols: int) -> dict:

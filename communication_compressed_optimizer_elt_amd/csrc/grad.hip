@@ -22,9 +22,12 @@ using demo::launch;
 using demo::overlap;
 using demo::status_of;
 
-constexpr uint32_t kWorkgroups = 2048;  // of a launch: 8 a CU
+// Copies up to this many bytes stay in the caches for who reads them next,
+// larger ones go past them.
+constexpr uint64_t kCached = (uint64_t)96 << 20;
 
-// a launch of at most this many elements is one workgroup's, without partial sums
+// A list of at most this many elements is one workgroup's, without partial sums:
+// norm and copy of 65536 11.7 us, of 131072 14.4 us (16.6 by one workgroup).
 constexpr uint64_t kSmall = 1u << 16;
 
 int check(uint32_t count, const demo_tensor* t) {
@@ -39,20 +42,25 @@ int check(uint32_t count, const demo_tensor* t) {
 
 uint64_t bytes_of(const demo_tensor& t) { return t.n_elems * elem_bytes(t.dtype); }
 
-// Elements of a chunk: at most 16384, fewer where that leaves workgroups
-// without work, more where a launch would have more than 2^31 chunks.
-uint32_t chunk_of(uint64_t elems) {
+// Elements of a chunk, which is a wave's: as few as 2048, but no more than `most`
+// chunks where `most` allows that many, and below 2^31 of them.
+uint32_t chunk_of(uint64_t elems, uint64_t most) {
     uint64_t chunk = 2048;
-    while (chunk < 16384 && elems / chunk > 2 * kWorkgroups) chunk *= 2;
-    while (elems / chunk >= (1u << 30)) chunk *= 2;
+    while (elems / chunk >= most) chunk *= 2;
     return (uint32_t)chunk;
 }
+// The norm's sums, one for four chunks, are added up by one workgroup: 32768
+// chunks (44 tensors of 268 million bf16: 349 us with the copy, 359 and 353 with
+// half and twice as many).  The copy has none: 2048 elements a wave (640 million
+// fp32 794 us, 882 in chunks of four times that).
+constexpr uint64_t kNormChunks = 1 << 15, kScaleChunks = 1 << 22;
 
 // f(arguments, their number of elements) for every launch: up to kTable tensors that hold something
 template <typename F>
-int each_launch(uint32_t count, const demo_tensor* src, const demo_tensor* dst, F f) {
+int each_launch(uint32_t count, const demo_tensor* src, const demo_tensor* dst, uint64_t most, F f) {
     for (uint32_t i = 0; i < count;) {
-        GradArgs a{};
+        GradArgs a;
+        a.count = 0;
         uint64_t elems = 0;
         uint32_t from = i;
         for (; i < count && a.count < kTable; i++) {
@@ -61,18 +69,18 @@ int each_launch(uint32_t count, const demo_tensor* src, const demo_tensor* dst, 
             a.count++;
         }
         if (!a.count) continue;
-        a.chunk = chunk_of(elems);
+        a.chunk = chunk_of(elems, most);
         a.count = 0;
         uint64_t chunks = 0;
         for (; from < i; from++) {
             const demo_tensor &x = src[from], &y = dst ? dst[from] : x;
             if (!x.n_elems) continue;
-            demo::TensorEntry& e = a.table[a.count++];
-            e.src = x.data;
-            e.dst = y.data;
-            e.n = x.n_elems;
-            e.first = (uint32_t)chunks;
-            e.kind = x.dtype | y.dtype << 2 | (aligned16(x.data) && aligned16(y.data) ? 16u : 0u);
+            const uint32_t k = a.count++;
+            a.src[k] = x.data;
+            a.dst[k] = y.data;
+            a.n[k] = x.n_elems;
+            a.first[k] = (uint32_t)chunks;
+            a.kind[k] = x.dtype | y.dtype << 2 | (aligned16(x.data) && aligned16(y.data) ? 16u : 0u);
             chunks += (x.n_elems + a.chunk - 1) / a.chunk;
         }
         a.chunks = (uint32_t)chunks;
@@ -81,23 +89,47 @@ int each_launch(uint32_t count, const demo_tensor* src, const demo_tensor* dst, 
     return DEMO_OK;
 }
 
-uint32_t grid_of(const GradArgs& a) { return std::min(a.chunks, kWorkgroups); }
+uint32_t grid_of(uint32_t chunks) { return (chunks + 3) / 4; }  // workgroups of four waves
 
 // sums of a norm's workgroups over all its launches; 0: one workgroup does it all
 uint64_t sums_of(uint32_t count, const demo_tensor* t) {
-    uint64_t sums = 0, launches = 0, total = 0;
-    each_launch(count, t, nullptr, [&](const GradArgs& a, uint64_t elems) {
-        sums += grid_of(a);
-        launches++;
+    uint64_t sums = 0, total = 0;
+    uint32_t launches = 0;
+    for (uint32_t i = 0; i < count; launches++) {
+        uint64_t elems = 0, chunks = 0;
+        uint32_t from = i, held = 0;
+        for (; i < count && held < kTable; i++)
+            if (t[i].n_elems) elems += t[i].n_elems, held++;
+        const uint32_t chunk = chunk_of(elems, kNormChunks);
+        for (; from < i; from++) chunks += (t[from].n_elems + chunk - 1) / chunk;
+        sums += grid_of((uint32_t)chunks);
         total += elems;
-        return (int)DEMO_OK;
-    });
+    }
     return launches <= 1 && total <= kSmall ? 0 : sums;
 }
 
 // whether what is written meets anything else that is read or written; a
 // tensor may be its own destination
 int disjoint(uint32_t count, const demo_tensor* src, const demo_tensor* dst, const void* sumsq, const float* norm) {
+    // The usual calls need no sorting: pieces that ascend, in place or all of them
+    // away from what is read.
+    uintptr_t end = 0, first = UINTPTR_MAX, src_first = UINTPTR_MAX, src_end = 0;
+    bool ascending = true, in_place = true;
+    for (uint32_t i = 0; i < count; i++) {
+        if (!dst[i].n_elems) continue;
+        const uintptr_t d = (uintptr_t)dst[i].data, s = (uintptr_t)src[i].data;
+        ascending = ascending && d >= end;
+        in_place = in_place && d == s;
+        first = std::min(first, d);
+        end = d + bytes_of(dst[i]);
+        src_first = std::min(src_first, s);
+        src_end = std::max(src_end, s + bytes_of(src[i]));
+    }
+    const auto apart = [](uintptr_t a0, uintptr_t a1, uintptr_t b0, uintptr_t b1) { return a1 <= b0 || b1 <= a0; };
+    const uintptr_t q = (uintptr_t)sumsq, r = (uintptr_t)norm;
+    if (ascending && (in_place || apart(first, end, src_first, src_end)) && apart(first, end, q, q + 8) &&
+        (!norm || (apart(first, end, r, r + 4) && apart(src_first, src_end, r, r + 4) && apart(q, q + 8, r, r + 4))))
+        return DEMO_OK;
     struct Span {
         uintptr_t from, to;
         bool written;
@@ -151,11 +183,11 @@ int demo_grad_norm(uint32_t count, const demo_tensor* tensors, double* sumsq, vo
     hipStream_t s = static_cast<hipStream_t>(hip_stream);
     double* partial = need ? static_cast<double*>(workspace) : sumsq;
     bool any = false;
-    const int rc = each_launch(count, tensors, nullptr, [&](GradArgs& a, uint64_t) {
+    const int rc = each_launch(count, tensors, nullptr, kNormChunks, [&](GradArgs& a, uint64_t) {
         any = true;
         a.partial = partial;
-        partial += grid_of(a);
-        return status_of(need ? launch(demo::grad_norm_kernel<4>, dim3(grid_of(a)), dim3(256), 0, s, a)
+        partial += grid_of(a.chunks);
+        return status_of(need ? launch(demo::grad_norm_kernel<4>, dim3(grid_of(a.chunks)), dim3(256), 0, s, a)
                               : launch(demo::grad_norm_kernel<16>, dim3(1), dim3(1024), 0, s, a));
     });
     if (rc || (any && !need)) return rc;
@@ -175,15 +207,19 @@ int demo_grad_clip(uint32_t count, const demo_tensor* src, const demo_tensor* ds
     if (!sumsq || !(max_norm >= 0.f)) return DEMO_EINVAL;
     if (!aligned_to(sumsq, 8) || !aligned_to(norm, 4)) return DEMO_EALIGN;
     if (const int rc = disjoint(count, src, dst, sumsq, norm)) return rc;
+    uint64_t bytes = 0;
+    for (uint32_t i = 0; i < count; i++) bytes += bytes_of(dst[i]);
+    const bool past = bytes > kCached;
     hipStream_t s = static_cast<hipStream_t>(hip_stream);
     const auto go = [&](GradArgs& a) {
         a.sumsq = sumsq;
         a.max_norm = max_norm;
         a.norm = norm;
         norm = nullptr;  // the first launch writes it
-        return status_of(launch(demo::grad_scale_kernel, dim3(std::max(grid_of(a), 1u)), dim3(256), 0, s, a));
+        return status_of(launch(past ? demo::grad_scale_kernel<true> : demo::grad_scale_kernel<false>,
+                                dim3(std::max(grid_of(a.chunks), 1u)), dim3(256), 0, s, a));
     };
-    if (const int rc = each_launch(count, src, dst, [&](GradArgs& a, uint64_t) { return go(a); })) return rc;
+    if (const int rc = each_launch(count, src, dst, kScaleChunks, [&](GradArgs& a, uint64_t) { return go(a); })) return rc;
     if (!norm) return DEMO_OK;
     GradArgs a{};  // no tensor holds anything: the norm alone
     return go(a);
