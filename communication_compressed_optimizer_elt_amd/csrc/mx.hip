@@ -67,7 +67,7 @@ hipError_t launch_quantize(const demo::MxArgs& a, bool wide, dim3 grid, hipStrea
 }
 
 // the kernel for few rows, and the columns that its grid holds (below 2^32 work-items)
-constexpr uint64_t kFewRows = 16, kFewRowsMaxCols = (uint64_t)1 << 26;
+constexpr uint64_t kFewRows = 16, kFewRowsMaxCols = (uint64_t)1 << 25;
 
 constexpr uint32_t kCus = 256;
 
@@ -83,6 +83,18 @@ struct Plan {
     uint32_t kb_split;
 };
 
+// The card runs 256 tiles of 256 x 256 at a time, 512 of 128 x 128 or 1024 of 64
+// x 64 (one, two and four workgroups a CU).  Measured:
+//  * a round of 256 tiles costs 1.6 rounds of 128 tiles (4096 x 4096 x 1024: 16.3
+//    against 18.3 us; 5120 x 5120 x 2048: 36.6 against 40.6; 4096 x 2048 x 2048, half
+//    a round: 24.9 against 17.1), so they are taken where rounds say so;
+//  * up to 256 tiles of 128, tiles of 64 fill the card better (1024 x 2048 x 2048:
+//    8.3 against 10.8 us), unless there are more than 192 of them with a sum of
+//    4096 or more (2048 x 2048 x 8192: 34.0 against 30.0; 300 x 10000 x 5000: 24.3
+//    against 20.7);
+//  * the sum is split where there are fewer than 512 workgroups, down to 10 steps
+//    (256 x 2048 x 8192: 15.9 us in 3, 18.8 in one, 16.7 in 2 or 4; 768 x 768 x
+//    16384: 22.0 in 3, 35.3 in one; 64 x 16384 x 4096: 12.7 in one, 14.5 in 2).
 Plan plan_of(uint64_t m, uint64_t n, uint64_t k) {
     const uint64_t kb = up(k, kStep) / kStep;
     if (m <= kFewRows && n <= kFewRowsMaxCols) return {0, 1, (uint32_t)kb};
@@ -90,7 +102,7 @@ Plan plan_of(uint64_t m, uint64_t n, uint64_t k) {
     const auto rounds = [](uint64_t count, uint64_t at_once) { return (count + at_once - 1) / at_once; };
     if (m >= 256 && n >= 256 && 33 * rounds(tiles(256), 256) <= 20 * rounds(tiles(128), 512))
         return {256, 1, (uint32_t)up(kb, 2)};
-    const uint64_t tile = tiles(128) > 256u ? 128 : 64, least = tile == 128 ? 32 : 8;
+    const uint64_t tile = tiles(128) > (kb >= 16 ? 192u : 256u) ? 128 : 64, least = tile == 128 ? 32 : 10;
     uint64_t splits = 512 / tiles(tile);
     if (splits > kb / least) splits = kb / least;
     if (splits < 1) splits = 1;
@@ -125,7 +137,12 @@ hipError_t launch_big(const demo::ProductArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_product(demo::ProductArgs a, const Plan& plan, void* workspace, hipStream_t s) {
-    if (plan.tile == 0) return launch(demo::mx_few_kernel<8>, dim3((a.n + 15) / 16), dim3(512), 0, s, a);
+    if (plan.tile == 0) {
+        // a wave a column, unless the columns are many and short (1 x 100352 x 2048: 27.0 us, 24.9 in the kernel for few rows)
+        if (a.m <= 2 && (a.kb > 8 || a.n <= 32768))
+            return launch(a.m == 1 ? demo::mx_rows_kernel<1> : demo::mx_rows_kernel<2>, dim3((a.n + 3) / 4), dim3(256), 0, s, a);
+        return launch(demo::mx_few_kernel<4>, dim3((a.n + 15) / 16), dim3(256), 0, s, a);
+    }
     a.kb_split = plan.kb_split;
     a.partial = plan.splits > 1 ? static_cast<float*>(workspace) : nullptr;
     a.tiles_m = (a.m + plan.tile - 1) / plan.tile;

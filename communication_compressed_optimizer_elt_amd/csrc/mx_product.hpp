@@ -661,23 +661,47 @@ __global__ __launch_bounds__(256, 1) void mx_stream_kernel(ProductArgs p) {
 }
 
 // Few rows: 16 columns of C for up to 16 rows by NW waves that share the sum
-// among them, each taking every NW-th step straight from memory.
+// among them, each taking every NW-th step straight from memory, eight steps' loads
+// under way at a time.  The waves' sums are added in their order.  Bound by the
+// latency of those loads: 16 x 2048 x 8192 takes 7.8 us (8.2 with one step's loads
+// and eight waves), 16 x 8192 x 2048 5.2, 16 x 100352 x 2048 32 us (3.6 TB/s; 40 us
+// where a load took 16 bytes of every 32), 8 x 4096 x 14336 10.3 to 12 us.
 template <int NW>
 __global__ __launch_bounds__(64 * NW) void mx_few_kernel(ProductArgs p) {
+    constexpr int U = 8;
     __shared__ __attribute__((aligned(16))) float sums[NW][16 * 20];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, row = lane & 15, g = lane >> 4;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), row = lane & 15, g = lane >> 4;
     const uint32_t n0 = blockIdx.x * 16;
     const uint32_t ra = min((uint32_t)row, p.m - 1), rb = min(n0 + row, p.n - 1);
-    const uint8_t *qa = p.a + (uint64_t)ra * p.pitch + g * 32, *xa = p.sa + (uint64_t)ra * p.s_pitch + g * 2;
-    const uint8_t *qb = p.b + (uint64_t)rb * p.pitch + g * 32, *xb = p.sb + (uint64_t)rb * p.s_pitch + g * 2;
+    // chunks g and 4 + g of a step: a load takes 64 bytes of a row
+    const uint8_t *qa = p.a + (uint64_t)ra * p.pitch + g * 16, *xa = p.sa + (uint64_t)ra * p.s_pitch;
+    const uint8_t *qb = p.b + (uint64_t)rb * p.pitch + g * 16, *xb = p.sb + (uint64_t)rb * p.s_pitch;
     v4f acc[1][1] = {};
-    for (uint32_t kb = wave; kb < p.kb; kb += NW) {
-        const uint32_t ea[1] = {*(const uint16_t*)(xa + kb * kStepScales)}, eb[1] = {*(const uint16_t*)(xb + kb * kStepScales)};
-        const v4i a0[1] = {*(const v4i*)(qa + kb * kStepK)}, a1[1] = {*(const v4i*)(qa + kb * kStepK + 16)};
-        const v4i b0[1] = {*(const v4i*)(qb + kb * kStepK)}, b1[1] = {*(const v4i*)(qb + kb * kStepK + 16)};
-        mx_multiply<0>(acc, a0, b0, ea, eb);
-        mx_multiply<1>(acc, a1, b1, ea, eb);
-    }
+    auto steps = [&](uint32_t kb, auto N) {
+        constexpr int n = decltype(N)::value;
+        uint2_v ea[n], eb[n];
+        v4i a[n][2][1], b[n][2][1];
+#pragma unroll
+        for (int u = 0; u < n; u++) {
+            const uint32_t k = kb + u * NW;
+            b[u][0][0] = *(const v4i*)(qb + k * kStepK), b[u][1][0] = *(const v4i*)(qb + k * kStepK + 64);
+            a[u][0][0] = *(const v4i*)(qa + k * kStepK), a[u][1][0] = *(const v4i*)(qa + k * kStepK + 64);
+            eb[u] = *(const uint2_v*)(xb + k * kStepScales);
+            ea[u] = *(const uint2_v*)(xa + k * kStepScales);
+        }
+#pragma unroll
+        for (int u = 0; u < n; u++)
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                const uint32_t x[1] = {ea[u][h] >> 8 * g}, y[1] = {eb[u][h] >> 8 * g};
+                mx_multiply<0>(acc, a[u][h], b[u][h], x, y);
+            }
+    };
+    uint32_t kb = wave;
+    for (; kb + (U - 1) * NW < p.kb; kb += U * NW) steps(kb, Int<U>());
+    if (kb + 3 * NW < p.kb) steps(kb, Int<4>()), kb += 4 * NW;
+    if (kb + NW < p.kb) steps(kb, Int<2>()), kb += 2 * NW;
+    if (kb < p.kb) steps(kb, Int<1>());
     *(v4f*)&sums[wave][row * 20 + 4 * g] = acc[0][0];
     __syncthreads();
     if (threadIdx.x < 32) {  // two lanes a row, eight columns each
@@ -689,6 +713,58 @@ __global__ __launch_bounds__(64 * NW) void mx_few_kernel(ProductArgs p) {
             for (int q = 0; q < 8; q++) v[q] += s[q];
         }
         finish8(p, r, n0 + c, 0, v);
+    }
+}
+
+// One or two rows, as a token at a time makes them: a wave for each column of C,
+// whose loads take 1 KB of it in one piece.  Lane l takes block l of 64 blocks of
+// 32 codes, of the rows and of the column alike, so the "rows" that the matrix
+// instruction multiplies are sixteen parts of the sum: their products are its
+// diagonal, and the rest of the result is nobody's.  Bound by the loads' latency
+// and, where there are many columns, by memory: one row x 2048 x 8192 takes 4.2 us
+// (mx_few_kernel 5.8), x 16384 x 8192 15.7 us (18.5; 4.5 TB/s); two or four columns
+// a wave 4.9 and 16.6 us, 5.7 and 17.6 us.
+template <int M>
+__global__ __launch_bounds__(256) void mx_rows_kernel(ProductArgs p) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t j = blockIdx.x * 4 + wave;
+    if (j >= p.n) return;
+    const uint8_t *qb = p.b + (uint64_t)j * p.pitch, *xb = p.sb + (uint64_t)j * p.s_pitch;
+    const uint32_t blocks = p.kb * kStepScales;
+    v4f acc[M][1] = {};
+    auto step = [&](uint32_t k, bool on) {  // matrix instructions heed no mask: what is off multiplies zeros
+        v4i a[M] = {}, b[1] = {};
+        uint32_t ea[M] = {}, eb[1] = {};
+        if (on) {
+            b[0] = *(const v4i*)(qb + k * 16);
+            eb[0] = xb[k];
+#pragma unroll
+            for (int i = 0; i < M; i++) {
+                a[i] = *(const v4i*)(p.a + (uint64_t)i * p.pitch + k * 16);
+                ea[i] = p.sa[(uint64_t)i * p.s_pitch + k];
+            }
+        }
+        mx_multiply<0>(acc, a, b, ea, eb);
+    };
+    uint32_t k0 = 0;
+    for (; k0 + 64 <= blocks; k0 += 64) step(k0 + lane, true);
+    if (k0 < blocks) step(k0 + lane, k0 + lane < blocks);
+    const int d = (lane & 15) - 4 * (lane >> 4);  // which of this lane's four sums is on the diagonal
+    float sum[M];
+#pragma unroll
+    for (int i = 0; i < M; i++) {
+        sum[i] = 0.f;
+#pragma unroll
+        for (int q = 0; q < 4; q++) sum[i] = d == q ? acc[i][0][q] : sum[i];
+#pragma unroll
+        for (int x = 32; x; x >>= 1) sum[i] += __shfl_xor(sum[i], x);
+    }
+    if (lane < M) {
+        float v[8] = {M > 1 && lane ? sum[M - 1] : sum[0]};
+        if (p.drop.on) drop8(p.drop, (uint64_t)lane * p.n + j, v);
+        if (p.dtype == kF32) put_row<float>(p, lane, j, 0, 1, v, false);
+        else if (p.dtype == kF16) put_row<f16_t>(p, lane, j, 0, 1, v, false);
+        else put_row<bf16_t>(p, lane, j, 0, 1, v, false);
     }
 }
 
