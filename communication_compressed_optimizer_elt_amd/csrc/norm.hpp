@@ -187,7 +187,7 @@ __global__ __launch_bounds__(64 * kNormWaves<W>) void norm_kernel(NormArgs p) {
         for (int v = 0; v < NV; v++)
 #pragma unroll
             for (int j = 0; j < 8; j++) sum = fmaf(h[v][j], h[v][j], sum);
-        const float r = 1.f / sqrtf(sum_row<W>(sum, part[turn], w) / (float)p.cols + p.eps);
+        const float r = rsqrtf(sum_row<W>(sum, part[turn], w) / (float)p.cols + p.eps);
         if (p.h) {
 #pragma unroll
             for (int v = 0; v < NV; v++) store_row8<WIDE>((T*)p.h + here * p.ld_h, c0 + v * W * 512, p.cols, h[v]);
@@ -358,9 +358,16 @@ __global__ __launch_bounds__(64 * W * kBackRows<W>) void norm_back_kernel(NormBa
             if (p.dres) next_res[v] = load_raw8<WIDE>((const T*)p.dres + row * p.ld_dres, c0 + v * W * 512, cols);
         }
     };
-    if (NV == 1) fetch();
+    auto fetch_weight = [&] {
 #pragma unroll
-    for (int v = 0; v < NV; v++) load_row8<WIDE>(p.w, c0 + v * W * 512, p.cols, weight[v]);
+        for (int v = 0; v < NV; v++) load_row8<WIDE>(p.w, c0 + v * W * 512, p.cols, weight[v]);
+    };
+    // Rows of two eighths a work-item have no registers to load the next one ahead in,
+    // and read w again (4096 x 16384 bf16 104 us; 125 with w kept, which spills), but
+    // where each value is a load of its own (285 us with w kept, 335 without).
+    constexpr bool kKeep = NV == 1 || !WIDE;
+    if (NV == 1) fetch();
+    if (kKeep) fetch_weight();
     int turn = 0;
     for (uint32_t first = blockIdx.x * kRows; first < p.rows; first += step, turn ^= 1) {
         const uint32_t here = row;
@@ -368,6 +375,7 @@ __global__ __launch_bounds__(64 * W * kBackRows<W>) void norm_back_kernel(NormBa
         float n[NV][8], g[NV][8], a[NV][8] = {}, sum = 0.f;
         const float r = on ? p.rstd[here] : 0.f;
         if (NV > 1) fetch();
+        if (!kKeep) fetch_weight();
 #pragma unroll
         for (int v = 0; v < NV; v++) {
             values8(next_h[v], n[v]);
@@ -417,14 +425,16 @@ __global__ __launch_bounds__(64 * W * kBackRows<W>) void norm_back_kernel(NormBa
 }
 
 // dw = addend + the workgroups' sums: 16 columns by 64 groups of them, each in
-// the order of the workgroups, then the groups in theirs.
+// the order of the workgroups, then the groups in theirs.  Added in 64 bits: 72
+// roundings in a row would be most of dw's error (1.7e-7 of its norm; so 6e-8),
+// and what bounds the kernel is its launch and one pass over the sums.
 constexpr int kJoinCols = 16;
 __global__ __launch_bounds__(1024) void norm_join_kernel(const float* partial, uint32_t count, uint32_t cols,
                                                          const float* addend, float* dw) {
     constexpr int kGroups = 1024 / kJoinCols;
-    __shared__ float sums[kGroups][kJoinCols + 1];
+    __shared__ double sums[kGroups][kJoinCols + 1];
     const uint32_t lane = threadIdx.x % kJoinCols, group = threadIdx.x / kJoinCols, c = blockIdx.x * kJoinCols + lane;
-    float sum = 0.f;
+    double sum = 0;
     if (c < cols) {
 #pragma unroll 8
         for (uint32_t i = group; i < count; i += kGroups) sum += partial[(uint64_t)i * cols + c];
@@ -432,10 +442,10 @@ __global__ __launch_bounds__(1024) void norm_join_kernel(const float* partial, u
     sums[group][lane] = sum;
     __syncthreads();
     if (group == 0 && c < cols) {
-        float s = 0.f;
+        double s = addend ? addend[c] : 0.f;
 #pragma unroll
         for (int i = 0; i < kGroups; i++) s += sums[i][lane];
-        dw[c] = addend ? addend[c] + s : s;
+        dw[c] = (float)s;
     }
 }
 
