@@ -66,6 +66,8 @@ hipError_t launch_quantize(const demo::MxArgs& a, bool wide, dim3 grid, hipStrea
                   grid, dim3(256), 0, s, a);
 }
 
+constexpr uint64_t kMaxSquares = (uint64_t)1 << 24;  // of 256 work-items: a grid has less than 2^32 of them
+
 // the kernel for few rows, and the columns that its grid holds (below 2^32 work-items)
 constexpr uint64_t kFewRows = 16, kFewRowsMaxCols = (uint64_t)1 << 25;
 
@@ -202,8 +204,10 @@ int demo_mx_quantize(const demo_mx_cfg* cfg, uint64_t rows, uint64_t cols, const
         a.s_pitch_t = (uint32_t)t.scale_pitch;
         a.tiles_r = (uint32_t)(t.pitch / 64);
     }
+    const uint64_t squares = (uint64_t)a.tiles_r * a.tiles_c;
+    if (squares >= kMaxSquares) return DEMO_EUNSUPPORTED;
     const bool wide = aligned16(src) && ld * eb % 16 == 0 && cols % 8 == 0;
-    const dim3 grid(a.tiles_r * a.tiles_c);
+    const dim3 grid((unsigned)squares);
     hipStream_t s = static_cast<hipStream_t>(hip_stream);
     return status_of(with_type(cfg->dtype, [&](auto type) {
         typedef decltype(type) T;

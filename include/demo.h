@@ -500,7 +500,8 @@ int demo_mx_layout(uint64_t rows, uint64_t cols, demo_operand *out);
  * magnitude within 6 * 2^e; codes are rounded to nearest even.  The format has
  * neither infinity nor NaN: a block with one of them has the scale byte 255 and
  * stands for NaN as a whole.  With dropout the values are first multiplied as
- * demo_dropout_backward does, in fp32 without a rounding between.
+ * demo_dropout_backward does, in fp32 without a rounding between.  At most 2^24
+ * - 1 squares of 128 x 128, padding counted (DEMO_EUNSUPPORTED beyond).
  */
 int demo_mx_quantize(const demo_mx_cfg *cfg, uint64_t rows, uint64_t cols, const void *src, uint64_t ld,
                      const demo_dropout_cfg *dropout, void *operand, void *operand_t, void *hip_stream);

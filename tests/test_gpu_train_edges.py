@@ -1,0 +1,189 @@
+"""Calls of the norm, the gradient's clipping and the 4-bit layer at the ends of
+what is allowed: offsets beyond 32 bits, subnormal squares, two threads at once,
+another current stream, one buffer in two places, replays beside eager calls.
+Results are equal to those of the same call with neighbouring rows or alone, which
+other tests hold against 64 bits."""
+import threading
+
+import pytest
+
+from communication_compressed_optimizer_elt_amd import binding as L
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def torch():
+    import torch
+
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    L.lib()
+    return torch
+
+
+def normal(torch, seed, *shape, dtype="float32"):
+    g = torch.Generator().manual_seed(seed)
+    return torch.randn(*shape, generator=g).to(getattr(torch, dtype)).cuda()
+
+
+def far_rows(torch, x, pitch):
+    """x again, its rows `pitch` elements apart."""
+    rows, cols = x.shape
+    y = torch.empty((rows - 1) * pitch + cols, dtype=x.dtype, device="cuda").as_strided((rows, cols), (pitch, 1))
+    return y.copy_(x)
+
+
+def block(torch, rows, cols):
+    return torch.zeros(L.demo_block_layout(rows, cols)["total_bytes"], dtype=torch.uint8, device="cuda")
+
+
+def packed(torch, seed, rows, cols):
+    q = torch.zeros(L.demo_mx_layout(rows, cols)["total_bytes"], dtype=torch.uint8, device="cuda")
+    L.demo_mx_quantize(L.Mx(), normal(torch, seed, rows, cols, dtype="bfloat16"), q)
+    return q
+
+
+@pytest.mark.parametrize("pitch", [(1 << 31) + 8, (1 << 31) + 9])
+def test_norm_of_far_rows(torch, pitch):
+    """Rows whose offsets in elements and in bytes pass 32 bits."""
+    x, w = normal(torch, 1, 3, 200, dtype="bfloat16"), normal(torch, 2, 200)
+    far = far_rows(torch, x, pitch)
+    outs = []
+    for m in (x, far):
+        y, q, qt, r = torch.empty_like(x), block(torch, 3, 200), block(torch, 200, 3), torch.empty(3, device="cuda")
+        dw, dx = torch.empty(200, device="cuda"), torch.empty_like(x)
+        L.demo_rms_norm(L.Norm(), m, w, y=y, rstd=r, operand=q, operand_t=qt)
+        ws = torch.empty(L.demo_rms_norm_workspace(L.Norm(), 3, 200), dtype=torch.uint8, device="cuda")
+        L.demo_rms_norm_backward(L.Norm(), x, m, w, r, dx, dresidual=m, dweight=dw, workspace=ws)
+        outs.append((y, q, qt, r, dw, dx))
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
+    L.demo_rms_norm(L.Norm(), x, w, y=far)
+    assert torch.equal(far, outs[0][0])
+
+
+def test_mx_of_far_rows(torch):
+    x = normal(torch, 1, 3, 200, dtype="bfloat16")
+    far = far_rows(torch, x, (1 << 31) + 8)
+    outs = []
+    for m in (x, far):
+        q, qt = (torch.zeros(L.demo_mx_layout(*s)["total_bytes"], dtype=torch.uint8, device="cuda") for s in ((3, 200), (200, 3)))
+        L.demo_mx_quantize(L.Mx(), m, q, qt)
+        outs.append((q, qt))
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
+    back = torch.empty_like(x)
+    L.demo_mx_dequantize(outs[0][0], back)
+    L.demo_mx_dequantize(outs[0][0], far)
+    assert torch.equal(back, far)
+
+
+@pytest.mark.parametrize("m,n,k,pitch", [(2100, 4104, 1024, (1 << 21) + 8), (2100, 4104, 1000, (1 << 21) + 8), (70, 80, 300, (1 << 26) + 1),
+                                         (2, 80, 300, (1 << 32) + 8), (9, 80, 300, (1 << 29) + 8), (64, 64, 16384, (1 << 26) + 8)])
+@pytest.mark.parametrize("add", [False, True])
+def test_products_into_far_rows(torch, m, n, k, pitch, add):
+    a, b = packed(torch, 1, m, k), packed(torch, 2, n, k)
+    ws = torch.empty(max(L.demo_mx_workspace(L.Mx(), m, n, k), 16), dtype=torch.uint8, device="cuda")
+    c = normal(torch, 3, m, n, dtype="bfloat16")
+    far = far_rows(torch, c, pitch)
+    for out in (c, far):
+        L.demo_mx_matmul(L.Mx(), m, n, k, a, b, out, addend=out if add else None, workspace=ws)
+    assert torch.equal(c, far)
+    del far
+
+
+@pytest.mark.parametrize("cols", [64, 512, 4096, 16384])
+def test_norm_of_subnormal_squares(torch, cols):
+    """Squares of 2^-140, whose sum and mean are exact, and eps 0: r is 2^70 to a step."""
+    x, w = torch.full((3, cols), 2.0**-70, device="cuda"), torch.ones(cols, device="cuda")
+    r, y = torch.empty(3, device="cuda"), torch.empty_like(x)
+    L.demo_rms_norm(L.Norm(eps=0.0), x, w, y=y, rstd=r)
+    assert ((r.double() / 2.0**70 - 1).abs() <= 2.0**-23).all()
+    assert ((y.double() - 1).abs() <= 2.0**-22).all()
+
+
+def test_one_operand_on_both_sides(torch):
+    """a b^T with b = a is symmetric: the same products, added in the same order."""
+    for m, k in ((40, 600), (600, 600), (2304, 1024)):
+        a = packed(torch, 1, m, k)
+        c, ws = torch.empty(m, m, device="cuda"), torch.empty(L.BLOCK_MAX_WORKSPACE, dtype=torch.uint8, device="cuda")
+        L.demo_mx_matmul(L.Mx(), m, m, k, a, a, c, workspace=ws)
+        assert torch.equal(c, c.t())
+
+
+def test_threads_on_streams_of_their_own(torch):
+    """Norm, backward pass and clipping by two threads at once, each with its workspace and outputs."""
+    rows, cols = 700, 1030
+    x, w = normal(torch, 1, rows, cols, dtype="bfloat16"), normal(torch, 2, cols)
+    g = L.Tensors([normal(torch, 3 + i, 30_000) for i in range(130)])
+
+    def outputs():
+        return (torch.empty_like(x), torch.empty(rows, device="cuda"), torch.empty_like(x), torch.empty(cols, device="cuda"),
+                torch.zeros(1, dtype=torch.float64, device="cuda"), torch.zeros(1, device="cuda"), torch.empty(130 * 30_000, device="cuda"))
+
+    def work(out, stream=None):
+        y, r, dx, dw, s, norm, flat = out
+        ws = torch.empty(L.demo_rms_norm_workspace(L.Norm(), rows, cols), dtype=torch.uint8, device="cuda")
+        wg = torch.empty(L.demo_grad_workspace(g), dtype=torch.uint8, device="cuda")
+        into = L.Tensors(flat.split(30_000))
+        for _ in range(10):
+            L.demo_rms_norm(L.Norm(), x, w, y=y, rstd=r, stream=stream)
+            L.demo_rms_norm_backward(L.Norm(), y, x, w, r, dx, dweight=dw, workspace=ws, stream=stream)
+            L.demo_grad_norm(g, s, workspace=wg, stream=stream)
+            L.demo_grad_clip(g, s, 1.0, dst=into, norm=norm, stream=stream)
+        (stream or torch.cuda.current_stream()).synchronize()
+
+    want, outs, errors = outputs(), [outputs() for _ in range(2)], []
+    work(want)
+
+    def run(out):
+        try:
+            work(out, torch.cuda.Stream())
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=run, args=(o,)) for o in outs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
+    for out in outs:
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+def test_replays_beside_eager_calls(torch):
+    """Every kernel of the list and of the norm in a graph that is replayed with eager calls between; what it reads changes."""
+    rows, cols = 300, 9000
+    x, w = normal(torch, 1, rows, cols, dtype="bfloat16"), normal(torch, 2, cols)
+    y, dx, r, dw = torch.empty_like(x), torch.empty_like(x), torch.empty(rows, device="cuda"), torch.empty(cols, device="cuda")
+    q, qt = block(torch, rows, cols), block(torch, cols, rows)
+    ws = torch.empty(L.demo_rms_norm_workspace(L.Norm(), rows, cols), dtype=torch.uint8, device="cuda")
+    grads = [torch.empty(5000, device="cuda") for _ in range(125)]
+    g, s, norm = L.Tensors(grads), torch.zeros(1, dtype=torch.float64, device="cuda"), torch.zeros(1, device="cuda")
+    wg = torch.empty(L.demo_grad_workspace(g), dtype=torch.uint8, device="cuda")
+
+    def work():
+        L.demo_rms_norm(L.Norm(), x, w, y=y, rstd=r, operand=q, operand_t=qt)
+        L.demo_rms_norm_backward(L.Norm(), y, x, w, r, dx, dweight=dw, workspace=ws)
+        L.demo_grad_norm(g, s, workspace=wg)
+        L.demo_grad_clip(g, s, 1.0, norm=norm)
+        return [t.clone() for t in (y, r, q, qt, dx, dw, s, norm, grads[0], grads[124])]
+
+    def inputs(i):
+        x.copy_(normal(torch, 10 + i, rows, cols, dtype="bfloat16"))
+        for j, t in enumerate(grads):
+            t.fill_(0.5 + i + j / 128)
+
+    inputs(0)
+    work()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        work()
+    for i in range(4):
+        inputs(i)
+        want = work()
+        inputs(i)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip((y, r, q, qt, dx, dw, s, norm, grads[0], grads[124]), want))

@@ -277,3 +277,9 @@ def test_binding_refuses_host_tensors():
                  lambda: L.demo_mx_matmul(L.Mx(), 16, 128, 16, u, u, x)):
         with pytest.raises(ValueError, match="device tensor"):
             call()
+
+
+def test_mx_quantize_refuses_grids_that_are_too_large():
+    """2^30 rows of one column are 2^23 squares, and as many beside them whose codes are padding."""
+    for rows, cols in ((2**30, 1), (2**30 - 127, 1)):
+        assert L.raw_mx_quantize(L.Mx().c(L.DTYPE_BF16), rows, cols, FAR, cols, None, 2**50, None) == L.EUNSUPPORTED
