@@ -114,10 +114,10 @@ Plan plan_of(uint64_t m, uint64_t n, uint64_t k) {
 // the partial sums of up to 512 tiles of 128 x 128
 static_assert(512 * 128 * 128 * 4 <= DEMO_BLOCK_MAX_WORKSPACE, "workspace");
 
-template <int TILE>
+template <int TILE, int STAGES>
 hipError_t launch_tiles(const demo::ProductArgs& a, dim3 grid, hipStream_t s) {
-    constexpr size_t lds = 2 * 2 * TILE * (demo::kStepK + 2 * demo::kStepScales);
-    return launch(demo::mx_kernel<TILE, TILE, 2, 2>, grid, dim3(256), lds, s, a);
+    constexpr size_t lds = 2 * TILE * (STAGES * demo::kStepK + demo::kMxPairs<STAGES> * 2 * demo::kStepScales);
+    return launch(demo::mx_kernel<TILE, TILE, 2, 2, STAGES>, grid, dim3(256), lds, s, a);
 }
 
 template <typename T>
@@ -150,8 +150,11 @@ hipError_t launch_product(demo::ProductArgs a, const Plan& plan, void* workspace
     a.tiles_m = (a.m + plan.tile - 1) / plan.tile;
     a.tiles_n = (a.n + plan.tile - 1) / plan.tile;
     const dim3 grid(a.tiles_m * a.tiles_n, plan.splits);
-    const hipError_t e = plan.tile == 64    ? launch_tiles<64>(a, grid, s)
-                         : plan.tile == 128 ? launch_tiles<128>(a, grid, s)
+    // where a CU has one workgroup at most, three steps' loads are under way instead of one
+    // (64 x 16384 x 4096: 10.4 us, 12.4 with two stages; 32 x 4096 x 4096: 9.5 and 11.3; but 512 x
+    // 6144 x 1024, three a CU, 9.2 and 7.3)
+    const hipError_t e = plan.tile == 64    ? grid.x * grid.y <= kCus ? launch_tiles<64, 4>(a, grid, s) : launch_tiles<64, 2>(a, grid, s)
+                         : plan.tile == 128 ? launch_tiles<128, 2>(a, grid, s)
                                             : launch_big(a, s);
     if (e != hipSuccess || plan.splits == 1) return e;
     const uint64_t blocks = ((uint64_t)a.m * ((a.n + 7) / 8) + 255) / 256;

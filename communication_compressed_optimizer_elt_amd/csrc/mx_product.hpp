@@ -80,18 +80,23 @@ __device__ __forceinline__ void mx_finish(const ProductArgs& p, const v4f (&acc)
     }
 }
 
-// BM x BN of C by WM x WN waves, one of the splits of the sum (grid y), loads
-// and stages as in product_kernel.  Scale bytes come 16 of a row at a time, for
-// two steps.
-template <int BM, int BN, int WM, int WN>
+// Places of two steps' scale bytes: of four stages three, as the steps from the one
+// that is read to the last one that is loaded may begin three pairs.
+template <int S>
+constexpr int kMxPairs = S == 4 ? 3 : 2;
+
+// BM x BN of C by WM x WN waves, one of the splits of the sum (grid y), loads as in
+// product_kernel, S stages.  Scale bytes come 16 of a row at a time, for two steps.
+template <int BM, int BN, int WM, int WN, int S>
 __global__ __launch_bounds__(64 * WM * WN) void mx_kernel(ProductArgs p) {
     constexpr int NW = WM * WN, SM = BM / WM / 16, SN = BN / WN / 16;
     constexpr int LA = BM / 8 / NW, LB = BN / 8 / NW;
     constexpr int kStage = (BM + BN) * kStepK, kScales = (BM + BN) * 2 * kStepScales;
     static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0 && BM % 64 == 0 && BN % 64 == 0 && (BM + BN) / 64 <= NW, "loads per wave");
-    static_assert(NW * finish_bytes<SM, SN>() <= 2 * kStage, "the way out fits the stages");
+    static_assert(S == 2 || S == 4, "a step's scale bytes behind it are none or one load");
+    static_assert(NW * finish_bytes<SM, SN>() <= S * kStage, "the way out fits the stages");
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-    const uint8_t* scales = lds + 2 * kStage;
+    const uint8_t* scales = lds + S * kStage;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     uint32_t tm, tn;
     tile_of(p.tiles_m, p.tiles_n, blockIdx.x, tm, tn);
@@ -114,33 +119,45 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_kernel(ProductArgs p) {
         const uint32_t r = 8 * (wave + i * NW) + (lane >> 3);
         ob[i] = min(r, p.n - 1 - n0) * p.pitch + ((lane & 7) ^ (r >> 1 & 7)) * 16;
     }
-    const bool scale_of_a = wave * 64 < BM;
+    const bool has_scales = wave < (BM + BN) / 64, scale_of_a = wave * 64 < BM;
     const uint32_t srow = scale_of_a ? min((uint32_t)(wave * 64 + lane), p.m - 1 - m0)
                                      : min((uint32_t)(wave * 64 - BM + lane), p.n - 1 - n0);
     const uint8_t* gs = scale_of_a ? p.sa + (uint64_t)m0 * p.s_pitch : p.sb + (uint64_t)n0 * p.s_pitch;
     const uint32_t os = srow * p.s_pitch;
 
+    int to = 0, to_pair = 0;  // what is filled next: the stage, and the place of two steps' scale bytes
     auto fetch = [&](uint32_t kb) {
-        const uint32_t at = lds0 + (kb & 1) * kStage;
+        const uint32_t at = lds0 + to * kStage;
 #pragma unroll
         for (int i = 0; i < LA; i++) load_lds16(ga + (uint64_t)kb * kStepK, oa[i], at + (wave + i * NW) * 1024);
 #pragma unroll
         for (int i = 0; i < LB; i++) load_lds16(gb + (uint64_t)kb * kStepK, ob[i], at + BM * kStepK + (wave + i * NW) * 1024);
-        if ((kb & 1) == 0 && wave < (BM + BN) / 64)  // two steps' scale bytes
-            load_lds16(gs + kb * kStepScales, os, lds0 + 2 * kStage + (kb >> 1 & 1) * kScales + wave * 1024);
+        if ((kb & 1) == 0) {
+            if (has_scales) load_lds16(gs + kb * kStepScales, os, lds0 + S * kStage + to_pair * kScales + wave * 1024);
+            to_pair = to_pair + 1 == kMxPairs<S> ? 0 : to_pair + 1;
+        }
+        to = to + 1 == S ? 0 : to + 1;
     };
 
     const int wm = wave % WM, wn = wave / WM, row = lane & 15, g = lane >> 4;
     const int c0 = ((2 * g) ^ (row >> 1)) * 16, c1 = ((2 * g + 1) ^ (row >> 1)) * 16;
     v4f acc[SM][SN] = {};
     uint32_t ea[SM], eb[SN];
-    fetch(kb0);
+    constexpr int kAfter = (S - 2) * (LA + LB);  // loads of a wave behind a step's own, its scale bytes aside
+    int from = 0, from_pair = 0;
+#pragma unroll
+    for (int s = 0; s < S - 1; s++)
+        if (kb0 + s < kb1) fetch(kb0 + s);
     for (uint32_t kb = kb0; kb < kb1; kb++) {
         // step kb has landed, and everyone has read the stage that is filled next
-        sync_loads<0>();
-        if (kb + 1 < kb1) fetch(kb + 1);
-        const uint8_t* stage = lds + (kb & 1) * kStage;
-        const uint8_t* sc = scales + (kb >> 1 & 1) * kScales + (kb & 1) * kStepScales + 2 * g;
+        if (S == 2 || kb + S - 2 >= kb1) sync_loads<0>();
+        else if (has_scales) sync_loads<kAfter + 1>();  // one of the two steps has some
+        else sync_loads<kAfter>();
+        if (kb + S - 1 < kb1) fetch(kb + S - 1);
+        const uint8_t* stage = lds + from * kStage;
+        const uint8_t* sc = scales + from_pair * kScales + (kb & 1) * kStepScales + 2 * g;
+        from = from + 1 == S ? 0 : from + 1;
+        if (kb & 1) from_pair = from_pair + 1 == kMxPairs<S> ? 0 : from_pair + 1;
 #pragma unroll
         for (int i = 0; i < SM; i++) ea[i] = *(const uint16_t*)(sc + ((wm * SM + i) * 16 + row) * 16);
 #pragma unroll

@@ -24,8 +24,8 @@ template __global__ void demo::grad_scale_kernel<true>(GradArgs);
 template __global__ void demo::mx_quantize_kernel<bf16_t, true, true, true>(MxArgs);
 template __global__ void demo::mx_quantize_kernel<float, false, false, false>(MxArgs);
 template __global__ void demo::mx_values_kernel<f16_t, true>(MxValuesArgs);
-template __global__ void demo::mx_kernel<64, 64, 2, 2>(ProductArgs);
-template __global__ void demo::mx_kernel<128, 128, 2, 2>(ProductArgs);
+template __global__ void demo::mx_kernel<64, 64, 2, 2, 4>(ProductArgs);
+template __global__ void demo::mx_kernel<128, 128, 2, 2, 2>(ProductArgs);
 template __global__ void demo::mx_big_kernel<void>(ProductArgs);
 template __global__ void demo::mx_stream_kernel<bf16_t, false>(ProductArgs);
 template __global__ void demo::mx_stream_kernel<float, true>(ProductArgs);
