@@ -36,21 +36,51 @@ __device__ __forceinline__ void mx_multiply(v4f (&acc)[SM][SN], const v4i (&fa)[
                                                                          Q, (int)eb[j], Q, (int)ea[i]);
 }
 
-// finish() of product.hpp, but fp32 results in aligned accesses leave in whole
-// lines: neighbouring lanes store 16 bytes each, where finish() stores 16 of every
-// 32 (8192 x 8192 x 2048: 114 us, 129 so).  The loads of the addend of 32 rows are
-// all in flight before the first sum.
+// A wave's way out in pieces of 32 rows, for fp32 results in aligned accesses:
+// neighbouring lanes take 16 bytes each, so that whole lines leave, where finish()
+// of product.hpp stores 16 of every 32 (8192 x 8192 x 2048: 114 us, 129 so).
 template <int SM, int SN>
+struct MxLines {
+    static constexpr int kRow = SN * 16 + 4, kLanes = SN * 4, kRows = 64 / kLanes, P = 32 / kRows;
+    static_assert(SM % 2 == 0 && P >= 1, "pieces of 32 rows");
+    v4f addend[P];
+
+    static __device__ __forceinline__ bool fits(const ProductArgs& p) { return p.dtype == kF32 && p.wide && !p.drop.on; }
+    // the addend of piece s, all loads in flight at once
+    __device__ __forceinline__ void load(const ProductArgs& p, int s, uint32_t i0, uint32_t j0, uint32_t lo_i, uint32_t lo_j, int lane) {
+        const uint32_t j = j0 + lane % kLanes * 4, top = i0 + s * 32 + lane / kLanes;
+#pragma unroll
+        for (int r = 0; r < P; r++) {
+            const uint32_t i = top + r * kRows;
+            addend[r] = v4f{};
+            if (p.addend && j >= lo_j && j < p.n && i >= lo_i && i < p.m)
+                addend[r] = *(const v4f*)((const float*)p.addend + i * p.ld_addend + j);
+        }
+    }
+    __device__ __forceinline__ void store(const ProductArgs& p, const float* slab, int s, uint32_t i0, uint32_t j0, uint32_t lo_i,
+                                          uint32_t lo_j, int lane) {
+        const uint32_t j = j0 + lane % kLanes * 4, top = i0 + s * 32 + lane / kLanes;
+#pragma unroll
+        for (int r = 0; r < P; r++) {
+            const uint32_t i = top + r * kRows;
+            const v4f v = *(const v4f*)(slab + (r * kRows + lane / kLanes) * kRow + lane % kLanes * 4) + addend[r];
+            if (j >= lo_j && j < p.n && i >= lo_i && i < p.m) __builtin_nontemporal_store(v, (v4f*)((float*)p.c + i * p.ldc + j));
+        }
+    }
+};
+
+// finish() of product.hpp, or by lines, each piece's addend loaded while the one
+// before is stored (3000 x 3000 x 3000 with an addend 33.0 us, 35.7 without).  EARLY:
+// `lines` holds the first piece's.
+template <int SM, int SN, bool EARLY = false>
 __device__ __forceinline__ void mx_finish(const ProductArgs& p, const v4f (&acc)[SM][SN], float* slab, uint32_t i0,
-                                          uint32_t j0, uint32_t lo_i, uint32_t lo_j, int lane) {
-    if (p.dtype != kF32 || !p.wide || p.drop.on) {
+                                          uint32_t j0, uint32_t lo_i, uint32_t lo_j, int lane, MxLines<SM, SN>& lines) {
+    typedef MxLines<SM, SN> Lines;
+    if (!Lines::fits(p)) {
         finish<SM, SN>(p, acc, slab, i0, j0, lo_i, lo_j, lane);
         return;
     }
-    constexpr int kRow = SN * 16 + 4, kLanes = SN * 4, kRows = 64 / kLanes, P = 32 / kRows;
-    static_assert(SM % 2 == 0 && P >= 1, "pieces of 32 rows");
-    const uint32_t j = j0 + lane % kLanes * 4;
-    const bool col = j >= lo_j && j < p.n;
+    if (!EARLY) lines.load(p, 0, i0, j0, lo_i, lo_j, lane);
 #pragma unroll 1
     for (int s = 0; s < SM / 2; s++) {
         pick<SM / 2>(s, [&](auto T) {
@@ -59,23 +89,13 @@ __device__ __forceinline__ void mx_finish(const ProductArgs& p, const v4f (&acc)
             for (int i = 0; i < 2; i++)
 #pragma unroll
                 for (int c = 0; c < SN; c++)
-                    *(v4f*)(slab + (i * 16 + (lane & 15)) * kRow + c * 16 + 4 * (lane >> 4)) = acc[t * 2 + i][c];
+                    *(v4f*)(slab + (i * 16 + (lane & 15)) * Lines::kRow + c * 16 + 4 * (lane >> 4)) = acc[t * 2 + i][c];
         });
         wave_lds_sync();
-        const uint32_t top = i0 + s * 32 + lane / kLanes;
-        v4f w[P];
-#pragma unroll
-        for (int r = 0; r < P; r++) {
-            const uint32_t i = top + r * kRows;
-            w[r] = v4f{};
-            if (p.addend && col && i >= lo_i && i < p.m) w[r] = *(const v4f*)((const float*)p.addend + i * p.ld_addend + j);
-        }
-#pragma unroll
-        for (int r = 0; r < P; r++) {
-            const uint32_t i = top + r * kRows;
-            const v4f v = *(const v4f*)(slab + (r * kRows + lane / kLanes) * kRow + lane % kLanes * 4) + w[r];
-            if (col && i >= lo_i && i < p.m) __builtin_nontemporal_store(v, (v4f*)((float*)p.c + i * p.ldc + j));
-        }
+        Lines next;
+        if (s + 1 < SM / 2) next.load(p, s + 1, i0, j0, lo_i, lo_j, lane);
+        lines.store(p, slab, s, i0, j0, lo_i, lo_j, lane);
+        lines = next;
         wave_lds_sync();
     }
 }
@@ -143,6 +163,15 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_kernel(ProductArgs p) {
     const int c0 = ((2 * g) ^ (row >> 1)) * 16, c1 = ((2 * g + 1) ^ (row >> 1)) * 16;
     v4f acc[SM][SN] = {};
     uint32_t ea[SM], eb[SN];
+    // a small tile's addend is loaded before anything else, and there at the end (2304 x
+    // 768 x 2561: 11.9 us, 10.7 so; of a tile of 128 it stands in the way: 4096 x 2048 x 2048 24.2, 26.3 so)
+    constexpr bool kEarly = SM == 2;
+    const uint32_t i0 = m0 + wm * SM * 16, j0 = n0 + wn * SN * 16;
+    MxLines<SM, SN> lines;
+    if constexpr (kEarly) {
+        const ProductArgs out = target(p, blockIdx.y);
+        if (MxLines<SM, SN>::fits(out)) lines.load(out, 0, i0, j0, 0, 0, lane);
+    }
     constexpr int kAfter = (S - 2) * (LA + LB);  // loads of a wave behind a step's own, its scale bytes aside
     int from = 0, from_pair = 0;
 #pragma unroll
@@ -177,8 +206,7 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_kernel(ProductArgs p) {
         mx_multiply<1>(acc, fa, fb, ea, eb);
     }
     __syncthreads();
-    mx_finish<SM, SN>(target(p, blockIdx.y), acc, (float*)(lds + wave * finish_bytes<SM, SN>()), m0 + wm * SM * 16,
-                   n0 + wn * SN * 16, 0, 0, lane);
+    mx_finish<SM, SN, kEarly>(target(p, blockIdx.y), acc, (float*)(lds + wave * finish_bytes<SM, SN>()), i0, j0, 0, 0, lane, lines);
 }
 
 // d += a b, 128 along the sum, with byte Q of the scale words
@@ -335,8 +363,9 @@ __global__ __launch_bounds__(256, 1) void mx_big_kernel(ProductArgs p) {
         asm volatile("" : "+a"(acc[i][0]), "+a"(acc[i][1]), "+a"(acc[i][2]), "+a"(acc[i][3]), "+a"(acc[i][4]),
                      "+a"(acc[i][5]), "+a"(acc[i][6]), "+a"(acc[i][7]));
     sync_loads<0>();
+    MxLines<8, 8> lines;
     mx_finish<8, 8>(p, acc, (float*)(lds + t.wave * finish_bytes<8, 8>()), t.m0 + t.wm * 128, t.n0 + t.wn * 128, t.lo_i,
-                 t.lo_j, t.lane);
+                    t.lo_j, t.lane, lines);
 }
 
 // The accumulators of mx_stream_kernel: acc[i][j] is a[4 (8 i + j)] to + 3, by
