@@ -81,6 +81,21 @@ __device__ __forceinline__ uint32_t mx_col(const PairSquare<T>& q, int j, float 
     return mx_four<T>(q.down(0, j), q.down(2, j), q.down(4, j), q.down(6, j), k);
 }
 
+// eight values from any element's address, `left` of them in the row; v is 0 before
+template <typename T>
+__device__ __forceinline__ void load_any(const T* src, uint32_t left, uint32_t (&v)[4]) {
+    if (left < 8) return load_each(src, left, v);
+    const uint4_v x = load16_any(src);
+#pragma unroll
+    for (int j = 0; j < 4; j++) v[j] = x[j];
+}
+__device__ __forceinline__ void load_any(const float* src, uint32_t left, float (&v)[8]) {
+    if (left < 8) return load_each(src, left, v);
+    const uint4_v x = load16_any(src), y = load16_any(src + 4);
+#pragma unroll
+    for (int j = 0; j < 4; j++) v[j] = __uint_as_float(x[j]), v[4 + j] = __uint_as_float(y[j]);
+}
+
 // WIDE: rows of src are 16-byte aligned and cols a multiple of 8.  DROP: the
 // source through a dropout's gradient, as fp32 from there on.
 template <typename T, bool TILE, bool DROP, bool WIDE>
@@ -115,7 +130,7 @@ __global__ __launch_bounds__(256, 4) void mx_quantize_kernel(MxArgs p) {
             for (int i = 0; i < 8; i++) {
 #pragma unroll
                 for (int j = 0; j < kWords; j++) sq.v[i][j] = 0;
-                if (r0 + i < p.rows && c0 < p.cols) load_each(src + (uint64_t)(r0 + i) * p.ld + c0, p.cols - c0, sq.v[i]);
+                if (r0 + i < p.rows && c0 < p.cols) load_any(src + (uint64_t)(r0 + i) * p.ld + c0, p.cols - c0, sq.v[i]);
             }
         }
     }
@@ -225,6 +240,8 @@ __global__ __launch_bounds__(256) void mx_values_kernel(MxValuesArgs p) {
         T* to = (T*)p.dst + r * p.ld + c;
         if (WIDE) {
             store8(to, v);
+        } else if (c + 8 <= p.cols) {
+            store8_any(to, v);
         } else {
 #pragma unroll
             for (int j = 0; j < 8; j++)

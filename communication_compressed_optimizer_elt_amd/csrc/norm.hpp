@@ -40,16 +40,15 @@ __device__ __forceinline__ Raw8<T> load_raw8(const T* row, uint32_t c, uint32_t 
     Raw8<T> r;
 #pragma unroll
     for (int j = 0; j < (int)sizeof(T) * 2; j++) r.w[j] = 0;
-    if (WIDE) {
-        if (c < cols) {
-            const uint4_v* from = (const uint4_v*)(row + c);
+    if (WIDE ? c < cols : c + 8 <= cols) {
 #pragma unroll
-            for (int i = 0; i < (int)sizeof(T) / 2; i++) {
-                const uint4_v x = from[i];
+        for (int i = 0; i < (int)sizeof(T) / 2; i++) {
+            const T* from = row + c + i * (16 / sizeof(T));
+            const uint4_v x = WIDE ? *(const uint4_v*)from : load16_any(from);
 #pragma unroll
-                for (int j = 0; j < 4; j++) r.w[i * 4 + j] = x[j];
-            }
+            for (int j = 0; j < 4; j++) r.w[i * 4 + j] = x[j];
         }
+    } else if (WIDE) {
     } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
         for (int j = 0; j < 8; j++)
@@ -78,6 +77,8 @@ template <bool WIDE, typename T>
 __device__ __forceinline__ void store_row8(T* row, uint32_t c, uint32_t cols, const float (&v)[8]) {
     if (WIDE) {
         if (c < cols) store8(row + c, v);
+    } else if (c + 8 <= cols) {
+        store8_any(row + c, v);
     } else {
 #pragma unroll
         for (int j = 0; j < 8; j++)
@@ -253,8 +254,8 @@ __global__ __launch_bounds__(256) void norm_turn_kernel(NormTurnArgs p) {
     float x[8][4], y[4][8], weight[4] = {}, r[8];
     const bool full = (tr + 1) * kBlk <= p.rows;
     const T* from = (const T*)p.h + r0 * p.ld_h + c0;
+    typedef T vec __attribute__((ext_vector_type(4)));
     if (WIDE && full) {
-        typedef T vec __attribute__((ext_vector_type(4)));
         vec w[8] = {};
         if (c0 < p.cols) {
 #pragma unroll
@@ -274,7 +275,16 @@ __global__ __launch_bounds__(256) void norm_turn_kernel(NormTurnArgs p) {
             const bool in = r0 + i < p.rows;
             r[i] = in ? p.rstd[r0 + i] : 0.f;
 #pragma unroll
-            for (int j = 0; j < 4; j++) x[i][j] = in && c0 + j < p.cols ? to_float(from[i * p.ld_h + j]) : 0.f;
+            for (int j = 0; j < 4; j++) x[i][j] = 0.f;
+            if (in && c0 + 4 <= p.cols) {
+                const vec v = load4_any(from + i * p.ld_h);
+#pragma unroll
+                for (int j = 0; j < 4; j++) x[i][j] = (float)v[j];
+            } else if (in) {
+#pragma unroll
+                for (int j = 0; j < 4; j++)
+                    if (c0 + j < p.cols) x[i][j] = to_float(from[i * p.ld_h + j]);
+            }
         }
 #pragma unroll
         for (int j = 0; j < 4; j++) weight[j] = c0 + j < p.cols ? p.w[c0 + j] : 0.f;
@@ -362,20 +372,16 @@ __global__ __launch_bounds__(64 * W * kBackRows<W>) void norm_back_kernel(NormBa
 #pragma unroll
         for (int v = 0; v < NV; v++) load_row8<WIDE>(p.w, c0 + v * W * 512, p.cols, weight[v]);
     };
-    // Rows of two eighths a work-item have no registers to load the next one ahead in,
-    // and read w again (4096 x 16384 bf16 104 us; 125 with w kept, which spills), but
-    // where each value is a load of its own (285 us with w kept, 335 without).
-    constexpr bool kKeep = NV == 1 || !WIDE;
-    if (NV == 1) fetch();
-    if (kKeep) fetch_weight();
+    // Rows of two eighths a work-item have no registers to load the next one ahead in, and
+    // read w again (4096 x 16384 bf16 104 us; 125 with w kept, which spills).
+    if (NV == 1) fetch(), fetch_weight();
     int turn = 0;
     for (uint32_t first = blockIdx.x * kRows; first < p.rows; first += step, turn ^= 1) {
         const uint32_t here = row;
         const bool on = here < p.rows;
         float n[NV][8], g[NV][8], a[NV][8] = {}, sum = 0.f;
         const float r = on ? p.rstd[here] : 0.f;
-        if (NV > 1) fetch();
-        if (!kKeep) fetch_weight();
+        if (NV > 1) fetch(), fetch_weight();
 #pragma unroll
         for (int v = 0; v < NV; v++) {
             values8(next_h[v], n[v]);
