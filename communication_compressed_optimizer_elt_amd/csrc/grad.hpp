@@ -9,6 +9,12 @@
 // nothing is copied to the device, and a captured call holds it.  A launch's
 // elements are cut into chunks that never cross a tensor; a chunk is a
 // wave's.
+//
+// Bound by bytes: the norm of 640 million fp32 takes 443 us (5.8 TB/s) and their
+// clipped copy 832 (6.2 TB/s); of 44 bf16 tensors of 268 million elements 102 us
+// (5.3 TB/s), the copy to fp32 248 (6.5 TB/s).  Small lists are bound by the host,
+// which fills the table (64 vectors of 2048: 15 us for the two calls, whose three
+// kernels take 11.7).
 #pragma once
 
 #include <hip/hip_runtime.h>
