@@ -150,11 +150,10 @@ constexpr int kNormWaves = W == 1 ? 4 : W;
 // Each row is read and written once, and a wave loads its part of the next row of
 // its workgroup before it works on this one.  Bound by bytes: 16384 x 2048 bf16 with
 // residual, h, statistics and an operand, 237 MB, takes 43 us (5.5 TB/s), 4096 x 8192
-// with y 48 us.  Eight columns a lane are 16 bytes of a 16-bit type and one piece of
-// the dropouts' and quantisers' cut; 512 columns a wave keep a row's waves few, so
-// that they meet rarely, and small calls on one wave.  Rows at any alignment take the
-// same accesses (WIDE: 16-byte aligned, columns a multiple of 8): 16384 x 2047
-// with y 81 us, 177 with one access a value.
+// with y 48 us.  Eight columns a lane are 16 bytes of a 16-bit type, and 16 lanes a
+// block of the operand.  Rows that are not WIDE (16-byte aligned, columns a multiple
+// of 8) take the same accesses at any alignment, but the last columns: 16384 x 2047
+// with y 81 us, 177 with an access for each value.
 template <typename T, int W, int NV, bool WIDE>
 __global__ __launch_bounds__(64 * kNormWaves<W>) void norm_kernel(NormArgs p) {
     constexpr uint32_t kRows = kNormWaves<W> / W;  // of a workgroup
