@@ -266,7 +266,7 @@ def lib() -> ctypes.CDLL:
         L.demo_rms_norm_backward.argtypes = [norm, U64, U64, P, U64, P, U64, P, P, P, U64, P, U64, P, P, P, U64, P]
         L.demo_grad_workspace.argtypes = [U32, tensors, ctypes.POINTER(U64)]
         L.demo_grad_norm.argtypes = [U32, tensors, P, P, U64, P]
-        L.demo_grad_clip.argtypes = [U32, tensors, tensors, P, ctypes.c_float, P, P]
+        L.demo_grad_clip.argtypes = [U32, tensors, tensors, P, ctypes.c_double, P, P]
         L.demo_mx_layout.argtypes = [U64, U64, ctypes.POINTER(demo_operand)]
         L.demo_mx_quantize.argtypes = [mx, U64, U64, P, U64, drop, P, P, P]
         L.demo_mx_dequantize.argtypes = [mx, U64, U64, P, P, U64, P]

@@ -195,7 +195,7 @@ int demo_grad_norm(uint32_t count, const demo_tensor* tensors, double* sumsq, vo
                             (uint32_t)sums, sumsq));
 }
 
-int demo_grad_clip(uint32_t count, const demo_tensor* src, const demo_tensor* dst, const double* sumsq, float max_norm,
+int demo_grad_clip(uint32_t count, const demo_tensor* src, const demo_tensor* dst, const double* sumsq, double max_norm,
                    float* norm, void* hip_stream) {
     if (!dst) dst = src;
     if (const int rc = check(count, src)) return rc;
@@ -204,7 +204,7 @@ int demo_grad_clip(uint32_t count, const demo_tensor* src, const demo_tensor* ds
         if (dst[i].n_elems != src[i].n_elems || (dst[i].dtype != src[i].dtype && dst[i].dtype != DEMO_DTYPE_F32) ||
             (dst[i].data == src[i].data && dst[i].dtype != src[i].dtype && src[i].n_elems))
             return DEMO_EINVAL;
-    if (!sumsq || !(max_norm >= 0.f)) return DEMO_EINVAL;
+    if (!sumsq || !(max_norm >= 0)) return DEMO_EINVAL;
     if (!aligned_to(sumsq, 8) || !aligned_to(norm, 4)) return DEMO_EALIGN;
     if (const int rc = disjoint(count, src, dst, sumsq, norm)) return rc;
     uint64_t bytes = 0;

@@ -36,7 +36,7 @@ struct GradArgs {
     uint32_t kind[kTable];   // type of src, 4 * type of dst, 16: both are 16-byte aligned
     uint32_t count, chunks;
     uint32_t chunk;          // elements of a chunk, a multiple of 2048
-    float max_norm;
+    double max_norm;
     const double* sumsq;     // scaled copy: S
     float* norm;             // scaled copy: sqrt(S) goes here (NULL: not wanted)
     double* partial;         // norm: a sum for each workgroup
@@ -161,7 +161,7 @@ __device__ __forceinline__ void scale_chunk(const S* x, D* y, uint32_t n, bool w
 
 template <bool PAST>
 __global__ __launch_bounds__(256) void grad_scale_kernel(GradArgs p) {
-    const double norm = sqrt(*p.sumsq), q = (double)p.max_norm / (norm + 1e-6);
+    const double norm = sqrt(*p.sumsq), q = p.max_norm / (norm + 1e-6);
     const float c = q >= 1.0 ? 1.f : (float)q;  // NaN stays NaN
     if (p.norm && blockIdx.x == 0 && threadIdx.x == 0) *p.norm = (float)norm;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);

@@ -456,6 +456,7 @@ int demo_grad_norm(uint32_t count, const demo_tensor *tensors, double *sumsq, vo
 /*
  * dst = c * src tensor by tensor, in fp32 and rounded once, with
  *   c = min(1, max_norm / (sqrt(*sumsq) + 1e-6)),
+ * in fp64 and rounded once to fp32,
  * and *norm = sqrt(*sumsq) (device float; NULL: not wanted).  dst holds as many
  * tensors of the same sizes, each of src's type or fp32: pieces of the flat fp32
  * gradient that demo_encode reads, for instance.  dst NULL: in place, and then
@@ -466,7 +467,7 @@ int demo_grad_norm(uint32_t count, const demo_tensor *tensors, double *sumsq, vo
  * steps reads *norm.
  */
 int demo_grad_clip(uint32_t count, const demo_tensor *src, const demo_tensor *dst, const double *sumsq,
-                   float max_norm, float *norm, void *hip_stream);
+                   double max_norm, float *norm, void *hip_stream);
 
 /*
  * The same linear layer on 4-bit operands: e2m1 codes (OCP microscaling; 0, 0.5,

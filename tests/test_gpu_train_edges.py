@@ -187,3 +187,12 @@ def test_replays_beside_eager_calls(torch):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip((y, r, q, qt, dx, dw, s, norm, grads[0], grads[124]), want))
+
+
+def test_limit_of_64_bits(torch):
+    """max_norm is not rounded to fp32: c is one rounding of the quotient of the doubles."""
+    g = torch.ones(4, device="cuda")
+    s, out = torch.tensor([4.0], dtype=torch.float64, device="cuda"), torch.empty(4, device="cuda")
+    for limit in (1.0 + 2.0**-25, 0.1, 1.0 / 3):
+        L.demo_grad_clip([g], s, limit, dst=[out])
+        assert torch.equal(out.cpu(), torch.full((4,), limit / (2.0 + 1e-6), dtype=torch.float64).float())
