@@ -61,7 +61,7 @@ __device__ __forceinline__ void stream8(T* p, const float (&v)[8]) {
     __builtin_nontemporal_store(a, (vec*)p);
 }
 
-// 16 bytes or four values from, and eight values to, any element's address: one access
+// 16 bytes, four or eight values from, and eight to, any element's address: one access
 // each (two for eight fp32 values), which the hardware splits where it has to
 typedef uint4_v uint4_any __attribute__((aligned(2)));
 template <typename T>
@@ -72,6 +72,17 @@ __device__ __forceinline__ auto load4_any(const T* p) {
     typedef uint2_v uint2_any __attribute__((aligned(2)));
     if constexpr (sizeof(T) == 4) return __builtin_bit_cast(vec, load16_any(p));
     else return __builtin_bit_cast(vec, (uint2_v)(*(const uint2_any*)p));
+}
+template <typename T>
+__device__ __forceinline__ void load8_any(const T* p, float (&v)[8]) {
+    constexpr int N = 16 / sizeof(T);
+    typedef T vec __attribute__((ext_vector_type(N)));
+#pragma unroll
+    for (int i = 0; i < 8; i += N) {
+        const vec a = __builtin_bit_cast(vec, load16_any(p + i));
+#pragma unroll
+        for (int j = 0; j < N; j++) v[i + j] = to_float(a[j]);
+    }
 }
 template <typename T>
 __device__ __forceinline__ void store8_any(T* p, const float (&v)[8]) {

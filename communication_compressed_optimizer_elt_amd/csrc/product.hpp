@@ -65,8 +65,8 @@ __device__ __forceinline__ void load_lds4(const uint8_t* base, uint32_t offset, 
     asm volatile("s_nop 0\n\tglobal_load_lds_dword %1, %2" ::"{m0}"(lds), "v"(offset), "s"(base) : "memory");
 }
 
-// C[i, j+from..j+7] from eight sums: drop, add, round once, store, element by
-// element or (wide, from 0, eight left) in aligned accesses
+// C[i, j+from..j+7] from eight sums: drop, add, round once, store: (wide) in aligned
+// accesses, all eight in accesses at any alignment, or element by element
 template <typename T>
 __device__ __forceinline__ void put_row(const ProductArgs& p, uint32_t i, uint32_t j, int from, int count, float (&v)[8],
                                         bool wide) {
@@ -80,6 +80,16 @@ __device__ __forceinline__ void put_row(const ProductArgs& p, uint32_t i, uint32
             for (int q = 0; q < 8; q++) v[q] += w[q];
         }
         store8(c, v);
+        return;
+    }
+    if (from == 0 && count == 8) {
+        if (p.addend) {
+            float w[8];
+            load8_any(add, w);
+#pragma unroll
+            for (int q = 0; q < 8; q++) v[q] += w[q];
+        }
+        store8_any(c, v);
         return;
     }
 #pragma unroll
