@@ -230,8 +230,8 @@ constexpr size_t kMxStreamLds = kMxBigLds + 4 * 4096;  // all that a CU has
 // instructions of half the length, two for each pair of fragments; the four of a
 // column's first half of the step stand before the four of the second, which add
 // to the same sums.
-// It takes what mx_stream_kernel does not: addends, dropouts, odd widths, three steps
-// or fewer.  2048 x 8192 x 8192 fp32 with an addend 79 to 90 us, 66 of them without
+// It takes what mx_stream_kernel does not: addends, dropouts, odd widths, an odd number
+// of steps, fewer than four.  2048 x 8192 x 8192 fp32 with an addend 79 to 90 us, 66 of them without
 // the addend's 67 MB, which are read when nothing multiplies; read ahead through LDS
 // that nobody uses they delay the steps' own loads (90.5 against 83.0 us).
 template <typename = void>

@@ -113,7 +113,7 @@ __device__ __forceinline__ void settle() {
 // results that all CUs write at the same time between two tiles.  Over cards and
 // runs 8192 x 8192 x 8192 takes 375 to 425 us (2.59 to 2.93 PFLOP/s), 4096 x 8192
 // x 2048 60 to 65 us, 2048 x 100352 x 2048 368 to 422 us; columns that are no
-// multiple of 8 are stored one by one (2048 x 50257 x 2048 331 us, 50256 220 us).
+// multiple of 8 are stored at any alignment (2048 x 50257 x 2048 264 us, 50256 220 us).
 // Loading the next tile's first blocks before the way out gave nothing (77.4
 // against 78.4 us), nor did two groups of 4 waves out of step (494 against 464
 // us).
