@@ -161,8 +161,9 @@ __device__ __forceinline__ void scale_chunk(const S* x, D* y, uint32_t n, bool w
 
 template <bool PAST>
 __global__ __launch_bounds__(256) void grad_scale_kernel(GradArgs p) {
-    const double norm = sqrt(*p.sumsq), q = p.max_norm / (norm + 1e-6);
-    const float c = q >= 1.0 ? 1.f : (float)q;  // NaN stays NaN
+    const double norm = sqrt(*p.sumsq), reach = norm + 1e-6;
+    // compared before divided: an infinite limit holds an infinite norm too; NaN stays NaN
+    const float c = p.max_norm >= reach ? 1.f : (float)(p.max_norm / reach);
     if (p.norm && blockIdx.x == 0 && threadIdx.x == 0) *p.norm = (float)norm;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     for (uint32_t b = blockIdx.x * 4 + wave; b < p.chunks; b += gridDim.x * 4) {

@@ -462,9 +462,9 @@ int demo_grad_norm(uint32_t count, const demo_tensor *tensors, double *sumsq, vo
  * gradient that demo_encode reads, for instance.  dst NULL: in place, and then
  * a gradient within max_norm is neither read nor written.  A tensor of dst may
  * be the same one of src (type too); otherwise what is written meets nothing
- * else.  max_norm >= 0, infinity included.  Infinities in the gradient make c 0
- * (and 0 * infinity is NaN), a NaN makes all of it NaN: a caller that skips such
- * steps reads *norm.
+ * else.  max_norm >= 0; at infinity c is 1 for every norm but NaN.  At any other
+ * limit infinities in the gradient make c 0 (and 0 * infinity is NaN); a NaN makes
+ * all of it NaN at every limit: a caller that skips such steps reads *norm.
  */
 int demo_grad_clip(uint32_t count, const demo_tensor *src, const demo_tensor *dst, const double *sumsq,
                    double max_norm, float *norm, void *hip_stream);
