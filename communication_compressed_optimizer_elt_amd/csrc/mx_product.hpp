@@ -378,8 +378,10 @@ __global__ __launch_bounds__(256, 1) void mx_big_kernel(ProductArgs p) {
 
 // The accumulators of mx_stream_kernel: acc[i][j] is a[4 (8 i + j)] to + 3, by
 // name.  Given variables, the compiler copies them where tiles follow one another
-// (it spilled 200 registers); no other value is in these registers, as the
-// compiler needs none of them and is told that all are written.
+// (it spilled 200 registers).  It is told that the kernel writes all of them, but
+// nothing it is told keeps it from putting a value there between two statements:
+// the build reads the kernel's assembly, and fails where one of them is named
+// outside these statements or anything is spilled.
 __device__ __forceinline__ void all_accumulators() {
     asm volatile("" ::: "a0", "a1", "a2", "a3", "a4", "a5", "a6", "a7", "a8", "a9", "a10", "a11", "a12", "a13",
                  "a14", "a15", "a16", "a17", "a18", "a19", "a20", "a21", "a22", "a23", "a24", "a25", "a26", "a27",
