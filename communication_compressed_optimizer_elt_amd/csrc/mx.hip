@@ -73,8 +73,10 @@ constexpr uint64_t kFewRows = 16, kFewRowsMaxCols = (uint64_t)1 << 25;
 
 constexpr uint32_t kCus = 256;
 
-// Results up to this many bytes stay in the caches for who reads them next,
-// larger ones go past them.
+// Results of mx_stream_kernel up to this many bytes stay in the caches for who reads
+// them next, larger ones go past them.  (The other tiles'
+// 16-bit results in aligned accesses, and fp32 ones through no dropout, go past them at
+// every size.)
 constexpr uint64_t kCached = (uint64_t)96 << 20;
 
 // How a product is cut: tiles of `tile` x `tile` and `splits` of the sum, or

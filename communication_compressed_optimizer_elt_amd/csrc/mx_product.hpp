@@ -38,7 +38,8 @@ __device__ __forceinline__ void mx_multiply(v4f (&acc)[SM][SN], const v4i (&fa)[
 
 // A wave's way out in pieces of 32 rows, for fp32 results in aligned accesses:
 // neighbouring lanes take 16 bytes each, so that whole lines leave, where finish()
-// of product.hpp stores 16 of every 32 (8192 x 8192 x 2048: 114 us, 129 so).
+// of product.hpp stores 16 of every 32 (8192 x 8192 x 2048: 114 us, 129 so).  They go
+// past the caches at every size, a split's partial sums too.
 template <int SM, int SN>
 struct MxLines {
     static constexpr int kRow = SN * 16 + 4, kLanes = SN * 4, kRows = 64 / kLanes, P = 32 / kRows;
@@ -514,8 +515,9 @@ constexpr int stream_early() {
 // lower ones behind those of the next tile's first half.  mx_big_kernel spends 12
 // us between two tiles, in which all CUs load or write and none multiplies: 4096
 // x 8192 x 2048 takes 45.5 us there and 36 here, 8192 x 8192 x 8192 230 and 217 to
-// 227 us (4.8 to 5.1 PFLOP/s; from registers the instructions reach 7.1 on random
-// codes and 9.4 on equal ones).
+// 227 us beside one another; over cards, and with what ran before, 217 to 266 (4.1 to
+// 5.1 PFLOP/s; from registers the instructions reach 7.1 on random codes and 9.4 on
+// equal ones).
 //
 // Bound by the clock that the matrix instructions' power leaves, and by the
 // moment when all CUs write: loads and stores come back in their order, so the
@@ -777,9 +779,10 @@ __global__ __launch_bounds__(64 * NW) void mx_few_kernel(ProductArgs p) {
 // 32 codes, of the rows and of the column alike, so the "rows" that the matrix
 // instruction multiplies are sixteen parts of the sum: their products are its
 // diagonal, and the rest of the result is nobody's.  Bound by the loads' latency
-// and, where there are many columns, by memory: one row x 2048 x 8192 takes 4.2 us
-// (mx_few_kernel 5.8), x 16384 x 8192 15.7 us (18.5; 4.5 TB/s); two or four columns
-// a wave 4.9 and 16.6 us, 5.7 and 17.6 us.
+// and, where there are many columns, by memory: calls back to back, one row x 2048 x 8192 takes
+// 4.2 us (mx_few_kernel 5.8), x 16384 x 8192 15.7 us (18.5); two or four columns a
+// wave 4.9 and 16.6 us, 5.7 and 17.6 us.  The kernel alone takes 3.6 and 12.5 us (5.7
+// TB/s).
 template <int M>
 __global__ __launch_bounds__(256) void mx_rows_kernel(ProductArgs p) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);

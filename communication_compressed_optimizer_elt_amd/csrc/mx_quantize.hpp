@@ -12,11 +12,11 @@
 // quantize_kernel.  A block of a row is then four neighbouring lanes, and the 32
 // rows of a column's block are one wave's: no maximum leaves its wave.
 //
-// Bound by the one or two rounds of workgroups that most matrices are, whose loads,
-// arithmetic and stores coincide: 8192 x 2048 fp32 as squares, both orientations,
-// takes 20.0 us (85 MB, 4.2 TB/s; waves wait to issue 67% of their time), 8192 x 2048
-// fp16 14.4 us (51 MB, 3.5 TB/s), 16384 x 8192 bf16 101 us (411 MB, 4.1 TB/s),
-// 16384 x 2047 bf16 24 us (41 with a load for each value).
+// Bound by issue: 8192 x 2048 fp32 as squares, both orientations, takes 20.0 us (85
+// MB, 4.2 TB/s; waves wait to issue 67% of their time), 8192 x 2048 fp16 14.4 us (51
+// MB, 3.5 TB/s; 47%).  More rounds of workgroups reach no higher rate: 16384 x 8192
+// bf16, 16 of them, 101 us (411 MB, 4.1 TB/s).  16384 x 2047 bf16 24 us where caches
+// hold the source (41 with a load for each value), 32 where they do not.
 #pragma once
 
 #include "quantize.hpp"

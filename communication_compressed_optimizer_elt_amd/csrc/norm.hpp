@@ -147,13 +147,14 @@ __device__ __forceinline__ uint2_v codes8(const float (&v)[8], float k) {
 template <int W>
 constexpr int kNormWaves = W == 1 ? 4 : W;
 
-// Each row is read and written once, and a wave loads its part of the next row of
-// its workgroup before it works on this one.  Bound by bytes: 16384 x 2048 bf16 with
-// residual, h, statistics and an operand, 237 MB, takes 43 us (5.5 TB/s), 4096 x 8192
-// with y 48 us.  Eight columns a lane are 16 bytes of a 16-bit type, and 16 lanes a
-// block of the operand.  Rows that are not WIDE (16-byte aligned, columns a multiple
-// of 8) take the same accesses at any alignment, but the last columns: 16384 x 2047
-// with y 81 us, 177 with an access for each value.
+// Each row is read and written once.  Where a workgroup has several rows, which is
+// beyond six waves a row or a million workgroups, a wave loads its part of the next one
+// before it works on this one (not of rows of two eighths a work-item).  Bound by
+// bytes: 16384 x 2048 bf16 with residual, h, statistics and an operand, 237 MB, takes 43
+// us (5.5 TB/s), 4096 x 8192 with y 48 us.  Eight columns a lane are 16 bytes of a
+// 16-bit type, and 16 lanes a block of the operand.  Rows that are not WIDE (16-byte
+// aligned, columns a multiple of 8) take the same accesses at any alignment, but the
+// last columns: 16384 x 2047 with y 81 to 87 us, 177 with an access for each value.
 template <typename T, int W, int NV, bool WIDE>
 __global__ __launch_bounds__(64 * kNormWaves<W>) void norm_kernel(NormArgs p) {
     constexpr uint32_t kRows = kNormWaves<W> / W;  // of a workgroup
@@ -388,7 +389,8 @@ __global__ __launch_bounds__(64 * W * kBackRows<W>) void norm_back_kernel(NormBa
         for (int v = 0; v < NV; v++) load_row8<WIDE>(p.w, c0 + v * W * 512, p.cols, weight[v]);
     };
     // Rows of two eighths a work-item have no registers to load the next one ahead in, and
-    // read w again (4096 x 16384 bf16 104 us; 125 with w kept, which spills).
+    // read w again (4096 x 16384 bf16 104 to 116 us, 125 with w kept).  They spill all the
+    // same, 2 to 5 registers of 128, at any alignment 10 to 12; w kept spills more.
     if (NV == 1) fetch(), fetch_weight();
     int turn = 0;
     for (uint32_t first = blockIdx.x * kRows; first < p.rows; first += step, turn ^= 1) {

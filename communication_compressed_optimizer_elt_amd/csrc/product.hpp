@@ -628,8 +628,9 @@ __global__ __launch_bounds__(256) void product_rows_kernel(ProductArgs p) {
 }
 
 // The splits' partial sums, added in their order, to the result.  They were
-// written just before and come from the caches; what this costs is in the
-// figures by which sums are split.
+// written just before (8-bit products leave them in the caches, 4-bit ones of aligned
+// rows do not); what this costs is in the figures by which sums are split.  Rows of odd
+// width are read value by value.
 template <typename = void>
 __global__ __launch_bounds__(256) void product_join_kernel(ProductArgs p, uint32_t splits) {
     const uint32_t groups = (p.n + 7) / 8;

@@ -395,9 +395,11 @@ typedef struct demo_norm_cfg {
  * there is a residual.  h and y may each be x or residual, in the same place
  * with the same pitch (y not x where operand_t is made from x); otherwise what
  * is written meets no other buffer of the call.  A row whose sum of squares
- * passes fp32's range has r = 0; with eps = 0 a row of zeros gives NaN.  1 <=
- * cols <= DEMO_NORM_MAX_COLS (DEMO_EUNSUPPORTED beyond), rows at most 2^30, rows
- * * cols at most DEMO_MAX_ELEMS.
+ * passes fp32's range has r = 0; with eps = 0 a row of zeros gives NaN.  The
+ * squares are fp32's at the lower end too, which shows where eps is below 2^-126:
+ * magnitudes below 2^-63 lose digits of r, and a row of 2^-75 or less has r
+ * infinite.  1 <= cols <= DEMO_NORM_MAX_COLS (DEMO_EUNSUPPORTED beyond), rows at most
+ * 2^30, rows * cols at most DEMO_MAX_ELEMS.
  */
 int demo_rms_norm(const demo_norm_cfg *cfg, uint64_t rows, uint64_t cols, const void *x, uint64_t ld_x,
                   const void *residual, uint64_t ld_residual, const float *weight, void *h, uint64_t ld_h, void *y,
@@ -413,8 +415,11 @@ int demo_rms_norm_workspace(const demo_norm_cfg *cfg, uint64_t rows, uint64_t co
  * dy*weight
  *   dx      = r * (g - n * mean over the row of g*n) + dresidual,
  *   dweight = addend + sum over the rows of dy*n,
- * dx being the gradient of x and of residual alike.  Sums in fp32, in an order
- * that the sizes fix; dx is rounded once to dtype.  dweight fp32 [cols] (NULL:
+ * dx being the gradient of x and of residual alike.  Sums in an order that the
+ * sizes fix: dx's in fp32, and it is rounded once to dtype; dweight's in fp32 over the
+ * rows of a workgroup, then in fp64.  dweight is within 2^-24 * ((R + 9) sum |dy*n| +
+ * |addend| + |dweight|), R = rows / 4096 up to 512 columns, / 2048 up to 1024, / 1024
+ * up to 2048, / 512 up to 4096 and / 256 beyond, rounded up.  dweight fp32 [cols] (NULL:
  * not wanted, and no workspace is needed); addend fp32 [cols], NULL or dweight
  * itself (to add to a gradient) among others.  dx may be dy, h or dresidual, in
  * the same place with the same pitch.  cfg->fmt and cfg->eps are not used.  The
@@ -520,7 +525,9 @@ int demo_mx_workspace(const demo_mx_cfg *cfg, uint64_t m, uint64_t n, uint64_t k
  * demo_block_matmul on 4-bit operands a (m x k) and b (n x k):
  *   c[i][j] = addend[i][j] + drop(sum over k of a[i][k]*b[j][k]),
  * with its rules for addend, dropout, pitches, overlaps, sizes and workspace.
- * Products are exact and sums are held in fp32 for every type of the result.
+ * Products are exact and sums are held in fp32 for every type of the result, with
+ * subnormal numbers.  A part of a sum that passes fp32's range is infinite, and a
+ * result NaN where such parts have both signs; what reaches below 2^-149 is lost.
  */
 int demo_mx_matmul(const demo_mx_cfg *cfg, uint64_t m, uint64_t n, uint64_t k, const void *a, const void *b, void *c,
                    uint64_t ldc, const void *addend, uint64_t ld_addend, const demo_dropout_cfg *dropout,
