@@ -214,12 +214,21 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_kernel(ProductArgs p) {
     mx_finish<SM, SN, kEarly>(target(p, blockIdx.y), acc, (float*)(lds + wave * finish_bytes<SM, SN>()), i0, j0, 0, 0, lane, lines);
 }
 
-// d += a b, 128 along the sum, with byte Q of the scale words
-template <int Q>
+// d += a b, 128 along the sum, with byte Q of the scale words.  WAIT: in steps with
+// branches, whose scale bytes the compiler masks in front of it; with a wait everywhere
+// 2048 x 8192 x 8192 with an addend takes 84.7 us, 81.9 so, and in mx_stream_kernel 8192
+// x 8192 x 8192 249 and 236.
+template <int Q, bool WAIT>
 __device__ __forceinline__ void mma4(v4f& d, const v4i& a, const v4i& b, uint32_t ea, uint32_t eb) {
-    asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[%5,%5,0] op_sel_hi:[0,0,0] cbsz:4 blgp:4"
-                 : "+a"(d)
-                 : "v"(a), "v"(b), "v"(ea), "v"(eb), "n"(Q));
+    if constexpr (WAIT)
+        asm volatile(DEMO_MFMA_WAIT
+                     "v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[%5,%5,0] op_sel_hi:[0,0,0] cbsz:4 blgp:4"
+                     : "+a"(d)
+                     : "v"(a), "v"(b), "v"(ea), "v"(eb), "n"(Q));
+    else
+        asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[%5,%5,0] op_sel_hi:[0,0,0] cbsz:4 blgp:4"
+                     : "+a"(d)
+                     : "v"(a), "v"(b), "v"(ea), "v"(eb), "n"(Q));
 }
 
 constexpr int kMxBigScales = 2 * kBig * 2 * kStepScales;  // of two steps
@@ -310,8 +319,8 @@ __global__ __launch_bounds__(256, 1) void mx_big_kernel(ProductArgs p) {
             for (int h = 0; h < 2; h++)
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
-                    if (h == 0) mma4<0>(acc[i][j], fb[j].half[0], fa[i].half[0], eb[j], ea[i]);
-                    else mma4<1>(acc[i][j], fb[j].half[1], fa[i].half[1], eb[j], ea[i]);
+                    if (h == 0) mma4<0, !decltype(STEADY)::value>(acc[i][j], fb[j].half[0], fa[i].half[0], eb[j], ea[i]);
+                    else mma4<1, !decltype(STEADY)::value>(acc[i][j], fb[j].half[1], fa[i].half[1], eb[j], ea[i]);
                     if constexpr (j >= 2) {
                         if (i == 0 && two) {
                             if (h == 0) load_first(kb + 2, Int<cur>(), Int<2 * (j - 2)>());
@@ -341,8 +350,8 @@ __global__ __launch_bounds__(256, 1) void mx_big_kernel(ProductArgs p) {
             for (int h = 0; h < 2; h++)
 #pragma unroll
                 for (int i = 4; i < 8; i++) {
-                    if (h == 0) mma4<0>(acc[i][j], fb[j].half[0], fa[i].half[0], eb[j], ea[i]);
-                    else mma4<1>(acc[i][j], fb[j].half[1], fa[i].half[1], eb[j], ea[i]);
+                    if (h == 0) mma4<0, !decltype(STEADY)::value>(acc[i][j], fb[j].half[0], fa[i].half[0], eb[j], ea[i]);
+                    else mma4<1, !decltype(STEADY)::value>(acc[i][j], fb[j].half[1], fa[i].half[1], eb[j], ea[i]);
                     if (h == 0 && i == 5 && !(j & 1) && two) load_second(kb + 2, Int<cur>(), Int<(j >> 1)>());
                     if ((j & 1) && i == 5) fa[j >> 1].half[h] = *(const v4i*)(la + nxt * kBigStage + (j >> 1) * 16 * kStepK + (h ? t.c1 : t.c0));
                     if ((j & 1) && h == 0 && i == 6) ea[j >> 1] = scale_bytes(sa, then, j >> 1);

@@ -19,6 +19,12 @@ constexpr size_t kBigLds = 2 * (kBigStage + kBigScales);
 
 __device__ __forceinline__ void fence_order() { __builtin_amdgcn_sched_barrier(0); }
 
+// A matrix instruction reads what a vector instruction wrote two wait states before it
+// and not less: the compiler sees to that for its own, but does not know one in a
+// statement, and may widen or mask an operand right in front of it.  Where it does,
+// the statement waits by itself; of the others the build makes sure in the assembly.
+#define DEMO_MFMA_WAIT "s_nop 1\n\t"
+
 // d += a b, 128 along the sum, at byte Q of the scale words
 template <int FMT_A, int FMT_B, int Q>
 __device__ __forceinline__ void mma8(v4f& d, const v8i& a, const v8i& b, uint32_t ea, uint32_t eb) {
@@ -259,7 +265,7 @@ __global__ __launch_bounds__(256, 1) void product_big_kernel(ProductArgs p) {
 // 890; the matrix units are busy for 68% of it.
 typedef float v16f __attribute__((ext_vector_type(16)));
 __device__ __forceinline__ void mma16(v16f& d, const v8b& a, const v8b& b) {
-    asm volatile("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+a"(d) : "v"(a), "v"(b));
+    asm volatile(DEMO_MFMA_WAIT "v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+a"(d) : "v"(a), "v"(b));
 }
 
 template <int FA, int FB>
