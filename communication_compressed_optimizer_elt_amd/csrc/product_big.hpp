@@ -261,8 +261,8 @@ __global__ __launch_bounds__(256, 1) void product_big_kernel(ProductArgs p) {
 // four waves before they widen the last step's codes and the others after.
 // Behind it the next block has landed, nobody reads this block's stage again,
 // and the loads of the block after the next go there.  8192 x 8192 x 8192 takes
-// 844 to 890 us (1.24 to 1.30 PFLOP/s), in tiles of 128 969 us on the card of the
-// 890; the matrix units are busy for 68% of it.
+// 789 to 890 us over cards (1.24 to 1.39 PFLOP/s), in tiles of 128 969 us on the card
+// of the 890; the matrix units are busy for 68% of it.
 typedef float v16f __attribute__((ext_vector_type(16)));
 __device__ __forceinline__ void mma16(v16f& d, const v8b& a, const v8b& b) {
     asm volatile(DEMO_MFMA_WAIT "v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+a"(d) : "v"(a), "v"(b));
